@@ -177,6 +177,77 @@ int pa_reshape_and_cache_decode(const void* key, const void* value, void* k_pool
                                 int64_t* slot_mapping, void* stream);
 
 /*
+ * pa_rope_and_cache -- pa_reshape_and_cache for models with rotary positions:
+ * per-head RMS norms of the queries and keys, the rotation of positions, and
+ * the write of K and V into their slots, in one pass over the projection's
+ * output.  The pages have no counterpart (they take q, k and v ready made).
+ * For every token i with s = slot_mapping[i] >= 0, and every head row x of
+ * query[i] and key[i]:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight       (only where a weight is given)
+ *   (y1, y2) -> (y1 c - y2 s, y2 c + y1 s)        for each of the R / 2 pairs of
+ *                                                 its first R = rotary_dim elements
+ *   query_out[i][h] = the query rows;  k_pool, v_pool at slot s = the key rows
+ *   and value[i], as pa_reshape_and_cache writes them.
+ * fp32 arithmetic, rounded once to dtype at the store; value rows are copied
+ * bit for bit.
+ *   query, key, value  rows of num_q_heads / num_kv_heads / num_kv_heads heads
+ *                 of head_dim elements (dtype), heads contiguous; tokens
+ *                 query_stride / key_stride / value_stride elements apart
+ *                 (multiples of 16 bytes, at least a row), so that the three
+ *                 may be slices of one projection's output
+ *   query_out     [num_tokens][num_q_heads][head_dim] (dtype); may be `query`
+ *                 itself when query_stride is num_q_heads * head_dim, and may
+ *                 overlap no other argument
+ *   slot_mapping  int64 [num_tokens]; negative = padding: nothing of the token
+ *                 is read or written.  Slots must be distinct within one call.
+ *   positions     int32 [num_axes][num_tokens], one position of each axis (one
+ *                 axis for text; time, height and width for images and video)
+ *   pair_axes     int32 [rotary_dim / 2], the axis each pair turns by, or NULL
+ *                 with one axis
+ *   cos_sin       float [max_position][rotary_dim]: row t holds the cosines of
+ *                 the rotary_dim / 2 pairs at position t, then their sines
+ *   rotary_dim    a multiple of 16, 16 .. head_dim
+ *   interleaved   0: pair p is elements (p, p + R / 2); 1: (2p, 2p + 1)
+ *   q_weight, k_weight  [head_dim] (dtype), or NULL for no norm of that side
+ * A token whose slot lies outside the pool, or with a position outside
+ * [0, max_position) or a pair axis outside [0, num_axes), is skipped whole and
+ * records PA_ERR_BAD_BLOCK_ID.  Launched with programmatic stream
+ * serialisation.
+ */
+int pa_rope_and_cache(const void* query, const void* key, const void* value, int64_t query_stride,
+                      int64_t key_stride, int64_t value_stride, void* query_out, void* k_pool,
+                      void* v_pool, const int64_t* slot_mapping, const int32_t* positions,
+                      int num_axes, const int32_t* pair_axes, const float* cos_sin,
+                      int64_t max_position, int rotary_dim, int interleaved, const void* q_weight,
+                      const void* k_weight, float eps, int64_t num_tokens, int num_q_heads,
+                      int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                      void* stream);
+
+/*
+ * pa_rope_and_cache_decode -- pa_rope_and_cache of one decode step, the slot
+ * taken from the block table as pa_reshape_and_cache_decode does: token b is
+ * position context_lens[b] - 1 of sequence b.
+ *   positions     int32 [num_axes][batch], or NULL with one axis and no
+ *                 pair_axes: context_lens[b] - 1
+ *   slot_mapping  int64 [batch] output, or NULL: the slot each token was
+ *                 written to, -1 where nothing was written
+ * Length 0 writes nothing (its query_out row too stays as it was).  A negative
+ * length, an unmapped position, a block outside [0, num_blocks) or a bad
+ * position writes nothing of the token and records PA_ERR_BAD_BLOCK_ID.  Other
+ * arguments as for pa_rope_and_cache.
+ */
+int pa_rope_and_cache_decode(const void* query, const void* key, const void* value,
+                             int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                             void* query_out, void* k_pool, void* v_pool,
+                             const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* positions, int num_axes,
+                             const int32_t* pair_axes, const float* cos_sin, int64_t max_position,
+                             int rotary_dim, int interleaved, const void* q_weight,
+                             const void* k_weight, float eps, int batch, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                             int dtype, int64_t* slot_mapping, void* stream);
+
+/*
  * pa_copy_blocks -- copy-on-write duplication of shared blocks ([P2] "Key
  * terms in this lesson", Copy-on-write: a block is shared until someone
  * writes to it, and the writer then gets a private copy; [P1] "Myths and
@@ -392,6 +463,120 @@ int pa_paged_attention_prefill(const void* q, const void* k_pool, const void* v_
                                int out_dtype, int batch, int num_q_heads, int num_kv_heads,
                                int head_dim, int64_t num_tokens, int64_t num_blocks, int kv_dtype,
                                void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Block-sparse decode attention.
+ *
+ * Over long contexts a query row may attend to a chosen part of its blocks:
+ * pa_update_key_bounds keeps a small summary of each block's keys,
+ * pa_block_scores scores every block of a row from it, pa_select_blocks keeps
+ * the best ones, and pa_paged_attention_decode_sparse attends to their tokens.
+ * The pages have no counterpart.  The calls need no workspace.  All four take
+ * PA_F32 and PA_BF16 and the shapes above, and are launched with programmatic
+ * stream serialisation.
+ *
+ * A query row r belongs to sequence seq_ids[r] (or r itself when seq_ids is
+ * NULL; several rows may name one sequence, for example a sequence's last
+ * tokens when several are verified at once) and sees its first context_lens[r]
+ * tokens.  Block j of a row is tokens j * block_size .. of its sequence; a row
+ * of length L has ceil(L / block_size) blocks, the last one maybe in part.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * pa_update_key_bounds -- for every block that holds new tokens, per kv head
+ * and channel the smallest and the largest key value over the block's tokens
+ * (those below the sequence's length; NaN keys give NaN):
+ *   key_bounds[blk][h][0][d] = min_t K[t][h][d],  [1][d] = max_t K[t][h][d].
+ *   key_bounds    [num_blocks][num_kv_heads][2][head_dim] (dtype); blocks
+ *                 without new tokens are left as they were
+ *   query_start   int32 [batch + 1], non-decreasing: the last query_start[b + 1]
+ *                 - query_start[b] tokens of sequence b are new (as for
+ *                 pa_paged_attention_prefill; equal to its length for the whole
+ *                 sequence, for example after a swap-in).  NULL: the last token
+ *                 of each sequence that has one.
+ *   max_query_len host-side upper bound of the new tokens of a sequence (sizes
+ *                 the grid); ignored when query_start is NULL
+ * The keys must already be in the pool.  A block with new tokens belongs to one
+ * sequence, or is full in every sequence that lists it.  A sequence whose
+ * length is negative or beyond its table, or with more new tokens than its
+ * length or than max_query_len, is skipped and records PA_ERR_BAD_BLOCK_ID; so
+ * is a block outside [0, num_blocks).
+ */
+int pa_update_key_bounds(const void* k_pool, void* key_bounds, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* query_start, int max_query_len, int batch, int num_kv_heads,
+                         int head_dim, int block_size, int64_t num_blocks, int dtype, void* stream);
+
+/*
+ * pa_block_scores -- an upper bound of <q, k> over each block's keys, the
+ * largest of a kv head's query heads:
+ *   scores[r][g][j] = max_{h of g} sum_d max(q[r][h][d] lo_d, q[r][h][d] hi_d)
+ * with lo, hi = key_bounds[table[j]][g], for the row's blocks j; scores past
+ * them are left as they were.  fp32 sums.  Bounds must be finite where a score
+ * matters (0 * inf gives NaN).
+ *   q             [num_rows][num_q_heads][head_dim] (dtype)
+ *   block_tables  int32 [batch][max_blocks_per_seq]
+ *   seq_ids       int32 [num_rows], or NULL (num_rows <= batch)
+ *   context_lens  int32 [num_rows]
+ *   max_context_len  host-side upper bound of context_lens (sizes the grid; at
+ *                 most max_blocks_per_seq * block_size)
+ *   scores        float [num_rows][num_kv_heads][score_stride], score_stride at
+ *                 least ceil(max_context_len / block_size)
+ * A row whose sequence lies outside [0, batch) or whose length is negative or
+ * above max_context_len is skipped, as is a block outside [0, num_blocks), and
+ * records PA_ERR_BAD_BLOCK_ID.
+ */
+int pa_block_scores(const void* q, const void* key_bounds, const int32_t* block_tables,
+                    int max_blocks_per_seq, const int32_t* seq_ids, const int32_t* context_lens,
+                    int max_context_len, int block_size, float* scores, int64_t score_stride,
+                    int64_t num_rows, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                    int64_t num_blocks, int dtype, void* stream);
+
+/*
+ * pa_select_blocks -- the max_selected blocks that each row and kv head
+ * attends to: its first num_first and last num_last blocks, then the others of
+ * the largest score (NaN counts as largest, equal scores go to the lower
+ * block); all of them when the row has no more.  The choice is exact and the
+ * same on every run.
+ *   scores        float [num_rows][num_kv_heads][score_stride]
+ *   context_lens  int32 [num_rows], at most max_context_len
+ *   selected      int32 [num_rows][num_kv_heads][max_selected] output: block
+ *                 numbers j in ascending order, -1 behind them
+ *   num_first + num_last <= max_selected.  With num_last >= 1 every row attends
+ *                 to the block of its own last token.
+ * A row whose length is negative or above max_context_len gets -1 throughout
+ * and records PA_ERR_BAD_BLOCK_ID.
+ */
+int pa_select_blocks(const float* scores, int64_t score_stride, const int32_t* context_lens,
+                     int max_context_len, int block_size, int32_t* selected, int max_selected,
+                     int num_first, int num_last, int64_t num_rows, int num_kv_heads, void* stream);
+
+/*
+ * pa_paged_attention_decode_sparse -- pa_paged_attention_decode over the
+ * tokens of chosen blocks only: with L = context_lens[r] and kv head g of query
+ * head h,
+ *   out[r][h] = sum_t softmax(scale * <q[r][h], K_t>)_t V_t
+ * over the tokens t < L of the blocks that selected[r][g] lists.
+ *   selected      int32 [num_rows][num_kv_heads][max_selected], in any order;
+ *                 a negative entry names no block, and a block listed twice
+ *                 counts twice
+ *   out           [num_rows][num_q_heads][head_dim], out_dtype PA_F32 or PA_BF16;
+ *                 a row that attends to nothing is zero
+ * Deterministic: no atomics, a fixed order of sums.  An entry at or past the
+ * row's blocks, or whose block lies outside [0, num_blocks), is skipped and
+ * records PA_ERR_BAD_BLOCK_ID; so is a row with a bad sequence or length
+ * (negative, or beyond its table), which gives zeros.  Other arguments as for
+ * pa_block_scores.
+ */
+int pa_paged_attention_decode_sparse(const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* seq_ids, const int32_t* context_lens,
+                                     const int32_t* selected, int max_selected, float scale,
+                                     int block_size, void* out, int out_dtype, int64_t num_rows,
+                                     int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int64_t num_blocks, int kv_dtype, void* stream);
 
 /*
  * pa_paged_attention_decode_contiguous -- the same attention over a

@@ -19,8 +19,10 @@ _BINDING_NAMES = (
     "pa_paged_attention_prefill", "pa_reshape_and_cache_decode", "pa_selftest_wait_timeout",
     "pa_paged_attention_decode_append", "pa_hbm_read_probe", "pa_paged_attention_decode_shared_prefix",
     "pa_paged_attention_shared_prefix_workspace_size",
+    "pa_rope_and_cache", "pa_rope_and_cache_decode",
+    "pa_update_key_bounds", "pa_block_scores", "pa_select_blocks", "pa_paged_attention_decode_sparse",
 )
-__all__ = list(_BINDING_NAMES) + ["decode_step"]
+__all__ = list(_BINDING_NAMES) + ["decode_step", "sparse_decode_step"]
 
 
 def __getattr__(name):
@@ -52,3 +54,42 @@ def decode_step(q, k_new, v_new, k_pool, v_pool, block_tables, context_lens, max
     b.pa_paged_attention_decode_append(q, k_new, v_new, k_pool, v_pool, block_tables, context_lens, max_context_len,
                                        scale, out, partition_size=partition_size, workspace=workspace,
                                        slot_mapping=slots, stream=stream)
+
+
+def sparse_decode_step(query, key, value, k_pool, v_pool, key_bounds, block_tables, context_lens, max_context_len,
+                       cos_sin, scale, query_out, scores, selected, out, positions=None, pair_axes=None,
+                       interleaved=False, q_weight=None, k_weight=None, eps=1e-6, num_first=1, num_last=2,
+                       slots=None, cow_pairs=None, stream=None):
+    """One decode step of one attention layer with rotary positions that
+    attends to selected.shape[2] blocks of each sequence:
+
+    1. copy_blocks for pending copy-on-write pairs (if any),
+    2. the new token's queries and keys normed (where weights are given) and
+       rotated, its K and V written to its slot (pa_rope_and_cache_decode),
+    3. the key bounds of the block it lies in (pa_update_key_bounds),
+    4. a score of every block and the choice of the best ones, the first
+       num_first and last num_last always among them (pa_block_scores,
+       pa_select_blocks),
+    5. attention over their tokens (pa_paged_attention_decode_sparse).
+
+    `query`, `key` and `value` are the projection's rows; `key_bounds` holds the
+    bounds of every block written before (pa_update_key_bounds after a prefill).
+    `query_out`, `scores` and `selected` are buffers that hold the step's
+    rotated queries, block scores and choice afterwards.  `context_lens` counts
+    the new token.
+    """
+    from . import _binding as b
+
+    with b._device_guard(stream, query, k_pool, v_pool, cow_pairs):
+        if cow_pairs is not None and cow_pairs.numel():
+            b.pa_copy_blocks(k_pool, v_pool, cow_pairs, stream=stream)
+        b.pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, cos_sin,
+                                   positions=positions, pair_axes=pair_axes, interleaved=interleaved, q_weight=q_weight,
+                                   k_weight=k_weight, eps=eps, slot_mapping=slots, stream=stream)
+        b.pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, stream=stream)
+        b.pa_block_scores(query_out, key_bounds, block_tables, context_lens, max_context_len, k_pool.shape[2], scores,
+                          stream=stream)
+        b.pa_select_blocks(scores, context_lens, max_context_len, k_pool.shape[2], selected, num_first=num_first,
+                           num_last=num_last, stream=stream)
+        b.pa_paged_attention_decode_sparse(query_out, k_pool, v_pool, block_tables, context_lens, selected, scale, out,
+                                           stream=stream)

@@ -45,6 +45,11 @@ inline bool supported_head_dim(int d) { return d == 64 || d == 128; }
 
 inline bool supported_block_size(int bs) { return bs == 8 || bs == 16 || bs == 32; }
 
+// Query heads of one kv head.
+inline bool supported_group(int g, int dtype) {
+    return g == 1 || g == 2 || g == 4 || g == 8 || (g == 16 && dtype == PA_BF16);
+}
+
 inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

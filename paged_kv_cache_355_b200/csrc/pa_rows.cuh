@@ -1,0 +1,74 @@
+// pa_rows.cuh -- head rows in registers: one lane holds 8 consecutive
+// elements of a row of head_dim elements, so head_dim / 8 lanes hold a row.
+// bf16 chunks are one 16-byte vector, fp32 chunks two.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr int kChunk = 8;  // elements a lane holds
+
+// Raw bits of one chunk.
+template <typename T>
+struct Chunk;
+
+template <>
+struct Chunk<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+    __device__ __forceinline__ void to_f32(float (&x)[kChunk]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16_lo_to_f32(w[i]);
+            x[2 * i + 1] = bf16_hi_to_f32(w[i]);
+        }
+    }
+    __device__ __forceinline__ void from_f32(const float (&x)[kChunk]) {
+        a.x = pack_bf16x2(x[0], x[1]);
+        a.y = pack_bf16x2(x[2], x[3]);
+        a.z = pack_bf16x2(x[4], x[5]);
+        a.w = pack_bf16x2(x[6], x[7]);
+    }
+};
+
+template <>
+struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        *reinterpret_cast<float4*>(p) = a;
+        *reinterpret_cast<float4*>(p + 4) = b;
+    }
+    __device__ __forceinline__ void to_f32(float (&x)[kChunk]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ void from_f32(const float (&x)[kChunk]) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+
+// Minimum and maximum that keep a NaN of either side.
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+}  // namespace pa
