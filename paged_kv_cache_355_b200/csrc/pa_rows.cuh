@@ -71,4 +71,40 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     return r;
 }
 
+// Sums over the LANES lanes of an aligned lane group of N values each
+// (N a power of two), left spread over the lanes: afterwards lane x of the
+// group holds the sums of values x * N / LANES + i in v[i], i < N / LANES, or,
+// where N < LANES, of value x * N / LANES in v[0] (the same in LANES / N lanes).
+// About N shuffles instead of N log2(LANES).
+template <int N, int LANES>
+__device__ __forceinline__ void reduce_scatter(float (&v)[N]) {
+    int n = N;
+#pragma unroll
+    for (int m = LANES / 2; m; m >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool upper = threadIdx.x & m;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i < n) {
+                    const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+        }
+    }
+}
+
+// 16 bytes from global to shared memory without a register, past L1; zeros
+// without a read where `in` is false.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 }  // namespace pa

@@ -9,6 +9,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "pa.h"
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -178,6 +181,367 @@ int launch_simt(const SparseParams& p, cudaStream_t st) {
     return PA_ERR_UNSUPPORTED;
 }
 
+// ---------------------------------------------------------------------------
+// bf16: matrix instructions
+// ---------------------------------------------------------------------------
+// A warp takes 16 tokens at a time (two half-tiles of 8, so that blocks of 8,
+// 16 and 32 tokens are all whole half-tiles) through a ring of shared memory of
+// its own, filled by asynchronous copies: warps never wait for one another
+// until the end.  Both products are m16n8k16 with the few query heads on the
+// 8-wide side: S^T = K Q^T over 16 tokens, O^T = V^T P^T over 16 channels at a
+// time, so no row of an instruction is padding.  P^T's fragment is S^T's
+// accumulator, rounded and transposed in 8x8 matrices between the lanes.
+// 16-byte chunk c of a row lies at c ^ (row & 7), so that the eight rows of a
+// matrix load touch all banks.
+// P is split into a bf16 value and a bf16 remainder (two products), so that
+// its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
+// once (2^-9) would be half of a bf16 output's own error.
+constexpr int kMmaWarps = 4;
+constexpr int kMaxSplits = 8;  // the portable cluster size
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A float of the shared memory of CTA `rank` of the cluster, at the address
+// that p has in this one.
+__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+    uint32_t at;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+
+// One cluster of `splits` CTAs per (row, kv head): its splits * 4 warps take
+// the tiles of the list in turn, each with its own running maximum and sum, and
+// the states are joined through the cluster's shared memory, so that a long
+// list of few rows fills the GPU without a workspace or a second launch.
+// NT: 8-wide tiles of query heads (2 for a group of 16).
+template <int D, int NT, int kStages>
+__global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const SparseParams p, int splits) {
+    constexpr int kHeads = 8 * NT;             // query heads, the group padded with zero rows
+    constexpr int kRowBytes = 2 * D;
+    constexpr int kTile = 16 * kRowBytes;      // K or V of one tile of 16 tokens
+    constexpr int kStage = 2 * kTile;
+    constexpr int kSteps = D / 16;
+    constexpr int kRowLanes = D / 8;           // lanes that copy one row
+    constexpr int kCopyRows = 32 / kRowLanes;  // rows of one copy instruction
+    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][K, V][16 tokens][D], later the states
+    __shared__ float s_m[kMmaWarps][kHeads], s_l[kMmaWarps][kHeads], c_m[kHeads], c_l[kHeads];
+    const float kNegInf = __int_as_float(0xff800000);
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t rank = splits > 1 ? cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / splits;
+    const int64_t row = unit / p.num_kv_heads;
+    const int h = (int)(unit - row * p.num_kv_heads);
+    const int group = p.num_q_heads / p.num_kv_heads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    // this warp's tiles, 16 at a time; lanes 2 i and 2 i + 1 look up the two
+    // half-tiles of the i-th.  The list is read one chunk ahead, the first time
+    // beside the row's length.
+    const int per_block = p.block_size / 8;  // half-tiles
+    const int shift = per_block == 1 ? 0 : per_block == 2 ? 1 : 2;
+    const int64_t halves = (int64_t)p.max_selected * per_block;
+    const int step = splits * kMmaWarps;     // warps of the cluster
+    const int64_t tiles = (halves + 1) / 2;
+    const int32_t* list = p.selected + unit * p.max_selected;
+    int64_t first = (int64_t)rank * kMmaWarps + warp;
+    int64_t half = (first + (int64_t)(lane >> 1) * step) * 2 + (lane & 1);
+    int entry = half < halves ? list[half >> shift] : -1;
+
+    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
+    const int L = p.context_lens[row];
+    const bool row_ok = seq >= 0 && seq < p.batch && L >= 0 && L <= (int64_t)p.max_blocks_per_seq * p.block_size;
+    if (!row_ok && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+    const int32_t* table = p.block_tables + (row_ok ? seq : 0) * p.max_blocks_per_seq;
+
+    // the lane's part of the copies: one chunk of one row in every kCopyRows
+    const int copy_row = lane / kRowLanes, copy_chunk = lane % kRowLanes;
+    const __nv_bfloat16* k_pool = static_cast<const __nv_bfloat16*>(p.k_pool) + copy_row * D + copy_chunk * 8;
+    const __nv_bfloat16* v_pool = static_cast<const __nv_bfloat16*>(p.v_pool) + copy_row * D + copy_chunk * 8;
+    const uint32_t slots = smem_addr(ring) + warp * (kStages * kStage);
+    const uint32_t copy_dst = slots + copy_row * kRowBytes + ((copy_chunk ^ copy_row) << 4);
+    // matrix loads: lane = (matrix, row).  K's matrices are (chunk of the
+    // k-step, half-tile), V's, transposed, (half-tile, chunk of the 16 channels)
+    const uint32_t mat_row = lane & 7, mat_lo = (lane >> 3) & 1, mat_hi = lane >> 4;
+    const uint32_t k_mat = slots + (mat_lo * 8 + mat_row) * kRowBytes + ((mat_hi ^ mat_row) << 4);
+    const uint32_t v_mat = slots + kTile + (mat_hi * 8 + mat_row) * kRowBytes + ((mat_lo ^ mat_row) << 4);
+
+    uint32_t q[NT][kSteps][2];  // head 8 n + g as a column of Q^T
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int head = 8 * n + g;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (row * p.num_q_heads + h * group + head) * D + 2 * t;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                q[n][i][c] = head < group ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c) : 0u;
+    }
+    float o[NT][kSteps][4] = {};     // channels 16 i + g (+ 8), heads 8 n + 2 t (+ 1)
+    float m[NT][2], l[NT][2] = {};   // of heads 8 n + 2 t (+ 1); l over this lane's tokens
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf;
+
+    for (; first < tiles && row_ok; first += (int64_t)step * 16) {
+        uint32_t at = 0;  // the half-tile's place in the pools, in rows of 8 tokens
+        int held = 0;     // its tokens below L
+        const int j = entry, sub = (int)(half & (per_block - 1));
+        half += (int64_t)step * 32;
+        entry = half < halves ? list[half >> shift] : -1;
+        if (j >= 0) {
+            int64_t blk = -1;
+            if ((int64_t)j * p.block_size < L) blk = table[j];
+            if (blk < 0 || blk >= p.num_blocks) {
+                record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+            } else {
+                held = min(8, max(0, L - j * p.block_size - 8 * sub));
+                at = (uint32_t)((blk * p.num_kv_heads + h) * per_block + sub);
+            }
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, held > 0);
+        todo = (todo | (todo >> 1)) & 0x55555555u;
+
+        auto fetch = [&](int lead, int stage) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int left = __shfl_sync(0xffffffffu, held, lead + a) - copy_row;
+                const size_t off = (size_t)__shfl_sync(0xffffffffu, at, lead + a) * (8 * D);
+#pragma unroll
+                for (int u = 0; u < 8 / kCopyRows; ++u) {
+                    const uint32_t dst = (copy_dst ^ ((u * kCopyRows) << 4)) + stage * kStage +
+                                         (a * 8 + u * kCopyRows) * kRowBytes;
+                    const bool in = u * kCopyRows < left;
+                    copy_async16(dst, k_pool + off + u * kCopyRows * D, in);
+                    copy_async16(dst + kTile, v_pool + off + u * kCopyRows * D, in);
+                }
+            }
+        };
+        unsigned ahead = todo;  // tiles still to be fetched
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) {
+            if (ahead) fetch(__ffs(ahead) - 1, st);
+            ahead &= ahead - 1;
+            copy_async_commit();
+        }
+        for (int stage = 0; todo; todo &= todo - 1, stage = stage + 1 == kStages ? 0 : stage + 1) {
+            const int lead = __ffs(todo) - 1;
+            copy_async_wait<kStages - 1>();
+            __syncwarp();  // every lane's copies are in
+            float s[NT][2][4] = {};  // tokens g, g + 8; heads 2 t, 2 t + 1; two chains
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t k[4];
+                ldmatrix_x4((k_mat ^ (i << 5)) + stage * kStage, k[0], k[1], k[2], k[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n][i & 1], k, q[n][i][0], q[n][i][1]);
+            }
+            const bool in0 = g < __shfl_sync(0xffffffffu, held, lead), in1 = g < __shfl_sync(0xffffffffu, held, lead + 1);
+
+            // p = 2^(x - m).  m is a maximum of earlier scores, not the running
+            // one: it moves only when a score passes it by 8, so that most tiles
+            // need no maximum across lanes and no rescale, and p stays below 2^8.
+            float x[NT][4];
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    x[n][c] = (c < 2 ? in0 : in1) ? (s[n][0][c] + s[n][1][c]) * p.scale_log2 : kNegInf;
+                    over |= x[n][c] > m[n][c & 1] + 8.f;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float top = fmaxf(m[n][c], fmaxf(x[n][c], x[n][c + 2]));
+#pragma unroll
+                        for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+                        const float keep = exp2_approx(m[n][c] - (top == kNegInf ? 0.f : top));
+                        m[n][c] = top;
+                        l[n][c] *= keep;
+#pragma unroll
+                        for (int i = 0; i < kSteps; ++i) {
+                            o[n][i][c] *= keep;
+                            o[n][i][c + 2] *= keep;
+                        }
+                    }
+            }
+            uint32_t hi[NT][2], lo[NT][2];  // P^T, tokens 0..7 and 8..15 of the tile
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float b0 = m[n][0] == kNegInf ? 0.f : m[n][0], b1 = m[n][1] == kNegInf ? 0.f : m[n][1];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const float p0 = exp2_approx(x[n][2 * a] - b0), p1 = exp2_approx(x[n][2 * a + 1] - b1);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    const uint32_t v = pack_bf16x2(p0, p1);
+                    hi[n][a] = movmatrix_trans(v);
+                    lo[n][a] = movmatrix_trans(pack_bf16x2(p0 - bf16_lo_to_f32(v), p1 - bf16_hi_to_f32(v)));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t v[4];
+                ldmatrix_x4_trans((v_mat ^ (i << 5)) + stage * kStage, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_bf16_16816(o[n][i], v, hi[n][0], hi[n][1]);
+                    mma_bf16_16816(o[n][i], v, lo[n][0], lo[n][1]);
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+            if (ahead) fetch(__ffs(ahead) - 1, stage);
+            ahead &= ahead - 1;
+            copy_async_commit();
+        }
+    }
+
+    // the warps' states, in the ring's place, joined to the CTA's; then the
+    // cluster's, each CTA finishing its share of the outputs
+    copy_async_wait<0>();
+    __syncthreads();
+    float(*s_o)[kHeads][D] = reinterpret_cast<float(*)[kHeads][D]>(ring);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int head = 8 * n + 2 * t + c;
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], y);
+            if (g == 0) {
+                s_m[warp][head] = m[n][c];
+                s_l[warp][head] = l[n][c];
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                s_o[warp][head][16 * i + g] = o[n][i][c];
+                s_o[warp][head][16 * i + g + 8] = o[n][i][c + 2];
+            }
+        }
+    __syncthreads();
+    const bool alone = splits == 1;
+    for (int i = threadIdx.x; i < group * D; i += kMmaWarps * 32) {
+        const int head = i / D, d = i % D;
+        float top = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s_m[w][head]);
+        const float base = top == kNegInf ? 0.f : top;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) {
+            const float weight = exp2f(s_m[w][head] - base);
+            sum = fmaf(s_l[w][head], weight, sum);
+            acc = fmaf(s_o[w][head][d], weight, acc);
+        }
+        if (alone) {
+            // nothing attended: a zero row (a NaN sum stays NaN)
+            store_out(p, (row * p.num_q_heads + h * group + head) * D + d, sum == 0.f ? 0.f : acc / sum);
+        } else {
+            s_o[0][head][d] = acc;  // read by this thread alone until here
+            if (d == 0) {
+                c_m[head] = top;
+                c_l[head] = sum;
+            }
+        }
+    }
+    if (alone) return;
+    cluster_sync();
+    for (int i = rank * (kMmaWarps * 32) + threadIdx.x; i < group * D; i += splits * (kMmaWarps * 32)) {
+        const int head = i / D, d = i % D;
+        float ms[kMaxSplits], ls[kMaxSplits], os[kMaxSplits];
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) {
+            ms[c] = c < splits ? load_cluster(&c_m[head], c) : kNegInf;
+            ls[c] = c < splits ? load_cluster(&c_l[head], c) : 0.f;
+            os[c] = c < splits ? load_cluster(&s_o[0][head][d], c) : 0.f;
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) top = fmaxf(top, ms[c]);
+        const float base = top == kNegInf ? 0.f : top;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) {
+            const float weight = exp2f(ms[c] - base);
+            sum = fmaf(ls[c], weight, sum);
+            acc = fmaf(os[c], weight, acc);
+        }
+        store_out(p, (row * p.num_q_heads + h * group + head) * D + d, sum == 0.f ? 0.f : acc / sum);
+    }
+    cluster_sync();  // the shared memory lives until the cluster has read it
+}
+
+template <int D, int NT>
+int launch_mma(const SparseParams& p, cudaStream_t st) {
+    constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB in flight a warp
+    constexpr size_t kSmem = (size_t)kMmaWarps * kStages * (D / 8) * 512;
+    static_assert(kSmem >= (size_t)kMmaWarps * NT * 8 * D * 4, "the states fit in the ring");
+    auto kernel = sparse_mma_kernel<D, NT, kStages>;
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+            return PA_ERR_CUDA;
+        configured.fetch_or(bit);
+    }
+    const int64_t units = p.num_rows * p.num_kv_heads;
+    // half-tiles are counted in 32 bits (a pool that needs more is 4 TB)
+    if (p.num_blocks > (1ll << 32) / (p.num_kv_heads * (p.block_size / 8))) return PA_ERR_UNSUPPORTED;
+    // One CTA a list keeps its four warps longest in their stream, and is best
+    // as soon as the lists fill the SMs: at 2048 lists of 64 blocks of 16 tokens
+    // 156 us (6.85 TB/s) against 165 with two CTAs and 190 with four; at 128
+    // lists 15.6 against 17.8 and 21.3.  Below that, as many as give each SM
+    // one (16 lists of 512 blocks: 72.8 us with one, 16.9 with eight); and three
+    // an SM, which is what its shared memory holds, where each warp then still
+    // has 16 tiles (128 lists of 256 blocks: 49.3 us with one, 47.6 with three).
+    const int64_t tiles = ((int64_t)p.max_selected * p.block_size + 15) / 16;
+    const int64_t fill = num_sms() / units, hold = 3 * num_sms() / units;
+    int64_t splits = std::max(fill, std::min(hold, tiles / (kMmaWarps * 16)));
+    splits = std::min(splits, std::min((int64_t)kMaxSplits, (tiles + kMmaWarps - 1) / kMmaWarps));
+    splits = std::max(splits, (int64_t)1);
+    if (units * splits > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.blockDim = dim3(kMmaWarps * 32);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, p, (int)splits) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    return launch_status();
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -225,7 +589,10 @@ extern "C" int pa_paged_attention_decode_sparse(const void* q, const void* k_poo
     p.err = error_word_ptr();
     if (!p.err) return PA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (kv_dtype == PA_BF16)
-        return head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(p, st) : launch_simt<__nv_bfloat16, 64>(p, st);
+    if (kv_dtype == PA_BF16) {
+        if (num_q_heads / num_kv_heads == 16)
+            return head_dim == 128 ? launch_mma<128, 2>(p, st) : launch_mma<64, 2>(p, st);
+        return head_dim == 128 ? launch_mma<128, 1>(p, st) : launch_mma<64, 1>(p, st);
+    }
     return head_dim == 128 ? launch_simt<float, 128>(p, st) : launch_simt<float, 64>(p, st);
 }
