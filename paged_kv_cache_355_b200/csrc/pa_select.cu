@@ -12,6 +12,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "pa.h"
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -128,90 +131,229 @@ struct ScoreParams {
     int64_t num_rows;
     int num_q_heads, num_kv_heads;
     int64_t num_blocks;
-    int tiles;  // CTAs along the blocks of one (row, kv head)
+    int chunks, tiles_per_warp;  // CTAs of one (row, kv head); tiles of 16 blocks of one warp
     int* err;
 };
 
-// The row's block table and its number of blocks; false (after recording the
-// error once, by `recorder`) where the sequence or the length is bad.
-__device__ __forceinline__ bool row_blocks(const int32_t* block_tables, const int32_t* seq_ids,
-                                           const int32_t* context_lens, int64_t row, int batch, int max_blocks_per_seq,
-                                           int64_t max_len, int block_size, bool recorder, int* err,
-                                           const int32_t*& table, int& blocks) {
-    const int64_t seq = seq_ids ? (int64_t)seq_ids[row] : row;
-    const int L = context_lens[row];
-    if (seq < 0 || seq >= batch || L < 0 || L > max_len) {
-        if (recorder) record_error(err, PA_ERR_BAD_BLOCK_ID);
-        return false;
-    }
-    table = block_tables + seq * max_blocks_per_seq;
-    blocks = (int)(((int64_t)L + block_size - 1) / block_size);
-    return true;
+// This warp's part of a (row, kv head): `tiles_per_warp` tiles of 16 blocks,
+// every kWarps-th, so that a short row still occupies all warps.
+struct WarpTiles {
+    const int32_t* table;
+    int64_t unit;  // row * num_kv_heads + kv head
+    int h, blocks, first, end;
+    bool named;    // the row's sequence exists
+};
+
+// Where the warp is, without the row's length: its table may be read beside it.
+__device__ __forceinline__ WarpTiles warp_tiles(const ScoreParams& p) {
+    WarpTiles w;
+    w.unit = blockIdx.x / p.chunks;
+    const int chunk = (int)(blockIdx.x - w.unit * p.chunks);
+    const int64_t row = w.unit / p.num_kv_heads;
+    w.h = (int)(w.unit - row * p.num_kv_heads);
+    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
+    w.named = seq >= 0 && seq < p.batch;
+    w.table = p.block_tables + (w.named ? seq : 0) * p.max_blocks_per_seq;
+    w.first = chunk * kWarps * p.tiles_per_warp + (threadIdx.x >> 5);
+    w.end = w.first + kWarps * p.tiles_per_warp;
+    w.blocks = 0;
+    return w;
 }
 
-constexpr int kScoreBlocksPerWarp = 16;
+// Block j's table entry, read whether or not the row is that long.
+__device__ __forceinline__ int32_t entry_of(const ScoreParams& p, const WarpTiles& w, int j) {
+    return w.named && j < p.max_blocks_per_seq ? w.table[j] : -1;
+}
 
-// CUDA-core form: D / 8 lanes hold one block's two rows, 8 channels each.
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) block_scores_kernel(const ScoreParams p) {
-    constexpr int kLanes = D / kChunk;
-    constexpr int kRows = 32 / kLanes;
+// The row's length, which ends the warp's tiles.
+__device__ __forceinline__ void end_tiles(const ScoreParams& p, WarpTiles& w) {
+    const int L = p.context_lens[w.unit / p.num_kv_heads];
+    if (!w.named || L < 0 || L > p.max_context_len) {
+        if (blockIdx.x % p.chunks == 0 && w.h == 0 && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+    } else {
+        w.blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
+    }
+    w.end = min(w.end, (w.blocks + 15) / 16);
+}
+
+// The physical block of the row's block j from its entry; -1 past the row's
+// blocks and (recorded) where it is bad.
+__device__ __forceinline__ int32_t block_of(const ScoreParams& p, const WarpTiles& w, int j, int32_t entry) {
+    if (j >= w.blocks) return -1;
+    if (entry < 0 || entry >= p.num_blocks) {
+        record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+        return -1;
+    }
+    return entry;
+}
+
+// bf16.  max(q lo, q hi) is q hi where q >= 0 and q lo where q < 0, so a score
+// is the dot product of (q-, q+) with (lo, hi) over 2 D terms, all of whose
+// products are exact: a matrix product (m16n8k16) of 16 blocks with the group's
+// heads, padded to 8 by repeats, which leave the maximum alone.  Bound by the
+// read of the bounds: a block's two rows are 4 D contiguous bytes, copied
+// asynchronously into a ring of two tiles that belongs to the warp alone.
+// 16-byte chunk c of block b lies at c ^ (b & 7), so that the eight rows of a
+// matrix load touch all banks.
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 3) block_scores_mma_kernel(const ScoreParams p) {
+    constexpr int kRowBytes = 4 * D;            // lo and hi of one block
+    constexpr int kTile = 16 * kRowBytes;
+    constexpr int kRowLanes = D / 4;            // lanes that copy one block
+    constexpr int kCopyRows = 32 / kRowLanes;
+    constexpr int kSteps = D / 16;
+    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][2][16 blocks][lo, hi]
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = blockIdx.x / p.tiles;
-    const int tile = (int)(blockIdx.x - unit * p.tiles);
-    const int64_t row = unit / p.num_kv_heads;
-    const int h = (int)(unit - row * p.num_kv_heads);
-    const int lane = threadIdx.x & 31;
-    const int sub = lane / kLanes, chunk = lane % kLanes;
-    const int32_t* table;
-    int blocks;
-    if (!row_blocks(p.block_tables, p.seq_ids, p.context_lens, row, p.batch, p.max_blocks_per_seq, p.max_context_len,
-                    p.block_size, tile == 0 && h == 0 && threadIdx.x == 0, p.err, table, blocks))
-        return;
-    const int first = (tile * kWarps + (threadIdx.x >> 5)) * kScoreBlocksPerWarp;
-    if (first >= blocks) return;
-    const int end = min(blocks, first + kScoreBlocksPerWarp);
+    WarpTiles w = warp_tiles(p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    // lane i: block i of a pair of tiles; e0 of the pair being multiplied, e1 of
+    // the one being fetched
+    int j = (w.first + (lane >> 4) * kWarps) * 16 + (lane & 15);
+    constexpr int kPair = 2 * kWarps * 16;  // blocks between a lane's blocks of two pairs
+    int32_t e0 = entry_of(p, w, j), e1 = entry_of(p, w, j + kPair);
+    end_tiles(p, w);
+    if (w.first >= w.end) return;
+    const int last = w.end * 16;  // blocks of other CTAs lie behind
+    e0 = j < last ? block_of(p, w, j, e0) : -1;
+    j += kPair;
+    e1 = j < last ? block_of(p, w, j, e1) : -1;
 
-    float q[G][kChunk];
+    const int64_t row = w.unit / p.num_kv_heads;
+    const int group = p.num_q_heads / p.num_kv_heads;
+    const int copy_row = lane / kRowLanes, copy_chunk = lane % kRowLanes;
+    const __nv_bfloat16* bounds = static_cast<const __nv_bfloat16*>(p.key_bounds) + (int64_t)w.h * 2 * D + 8 * copy_chunk;
+    const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
+    const uint32_t slots = smem_addr(ring) + warp * (2 * kTile);
+    const uint32_t copy_dst = slots + copy_row * kRowBytes;
+    auto fetch = [&](int32_t e, int half, int stage) {  // one tile: lanes 16 half .. of e
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        Chunk<T> raw;
-        raw.load(static_cast<const T*>(p.q) + ((row * p.num_q_heads + h * G + g) * D) + chunk * kChunk);
-        raw.to_f32(q[g]);
-    }
-    float* out = p.scores + unit * p.score_stride;
-    for (int base = first; base < end; base += kRows) {
-        const int j = base + sub;
-        bool ok = j < end;
-        int64_t blk = -1;
-        if (ok) {
-            blk = table[j];
-            if (blk < 0 || blk >= p.num_blocks) {
-                record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-                ok = false;
+        for (int u = 0; u < 16; u += kCopyRows) {
+            const int32_t blk = __shfl_sync(0xffffffffu, e, 16 * half + u + copy_row);
+            const uint32_t dst = copy_dst + stage * kTile + u * kRowBytes + ((copy_chunk ^ ((u + copy_row) & 7)) << 4);
+            copy_async16(dst, bounds + (blk < 0 ? 0 : blk) * block_stride, blk >= 0);
+        }
+    };
+    fetch(e0, 0, 0);
+    copy_async_commit();
+    if (w.first + kWarps < w.end) fetch(e0, 1, 1);
+    copy_async_commit();
+
+    uint32_t q[2][NT][kSteps][2];  // negative and other values of head 8 n + g
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int head = w.h * group + (8 * n + g) % group;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (row * p.num_q_heads + head) * D + 2 * t;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c);
+                uint32_t neg;  // the sign of each half, all over it
+                asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(x));
+                q[0][n][i][c] = x & neg;
+                q[1][n][i][c] = x & ~neg;
             }
-        }
-        float lo[kChunk] = {}, hi[kChunk] = {};
-        if (ok) {
-            const T* src = static_cast<const T*>(p.key_bounds) + ((blk * p.num_kv_heads + h) * 2) * D + chunk * kChunk;
-            Chunk<T> raw;
-            raw.load(src);
-            raw.to_f32(lo);
-            raw.load(src + D);
-            raw.to_f32(hi);
-        }
-        float best = __int_as_float(0xff800000);
+    }
+    // matrix loads: lane = (matrix, row), the matrices (8 blocks, chunk of 8 channels)
+    const uint32_t mat_row = lane & 7, mat_lo = (lane >> 3) & 1, mat_hi = lane >> 4;
+    const uint32_t mat = slots + (mat_lo * 8 + mat_row) * kRowBytes + ((mat_hi ^ mat_row) << 4);
+    float* out = p.scores + w.unit * p.score_stride;
+    int half = 0;
+    for (int tile = w.first; tile < w.end; tile += kWarps, half ^= 1) {
+        copy_async_wait<1>();
+        __syncwarp();  // every lane's copies are in
+        float s[2][NT][4] = {};
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float sum = 0.f;
+        for (int side = 0; side < 2; ++side)
 #pragma unroll
-            for (int e = 0; e < kChunk; ++e) sum = fmaf(q[g][e], q[g][e] < 0.f ? lo[e] : hi[e], sum);
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t a[4];
+                ldmatrix_x4((mat ^ (i << 5)) + half * kTile + side * 2 * D, a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int m = kLanes / 2; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            best = max_nan(best, sum);
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[side][n], a, q[side][n][i][0], q[side][n][i][1]);
+            }
+        __syncwarp();  // every lane has read the stage
+        const unsigned have = __ballot_sync(0xffffffffu, e0 >= 0) >> (16 * half);
+        if (tile + 2 * kWarps < w.end) fetch(e1, half, half);
+        copy_async_commit();
+        if (half == 1) {
+            e0 = e1;
+            j += kPair;
+            e1 = j < last ? block_of(p, w, j, entry_of(p, w, j)) : -1;
         }
-        if (ok && chunk == 0) out[j] = best;
+        // heads 2 t, 2 t + 1 (+ 8) of blocks g and g + 8
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            float best = max_nan(s[0][0][2 * a] + s[1][0][2 * a], s[0][0][2 * a + 1] + s[1][0][2 * a + 1]);
+            if (NT == 2)
+                best = max_nan(best, max_nan(s[0][NT - 1][2 * a] + s[1][NT - 1][2 * a],
+                                             s[0][NT - 1][2 * a + 1] + s[1][NT - 1][2 * a + 1]));
+            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            if (t == a && (have >> (g + 8 * a) & 1)) out[tile * 16 + g + 8 * a] = best;
+        }
+    }
+    copy_async_wait<0>();
+}
+
+// fp32, on the CUDA cores: D / 4 lanes hold the two rows of a block, four
+// channels each, four blocks at a time; their sums over the lanes by one
+// reduce-scatter.
+template <int D, int G>
+__global__ void __launch_bounds__(kWarps * 32) block_scores_f32_kernel(const ScoreParams p) {
+    constexpr int kLanes = D / 4;
+    constexpr int kRows = 32 / kLanes;    // blocks side by side
+    constexpr int kBlocks = 4;            // blocks of one lane
+    griddep_wait();
+    griddep_launch_dependents();
+    WarpTiles w = warp_tiles(p);
+    end_tiles(p, w);
+    if (w.first >= w.end) return;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, x = lane % kLanes;
+    const int64_t row = w.unit / p.num_kv_heads;
+    float4 q[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        q[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                                (row * p.num_q_heads + w.h * G + i) * D + 4 * x);
+    const float* bounds = static_cast<const float*>(p.key_bounds) + (int64_t)w.h * 2 * D + 4 * x;
+    const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
+    float* out = p.scores + w.unit * p.score_stride;
+    for (int tile = w.first; tile < w.end; tile += kWarps) {
+        for (int j0 = tile * 16 + sub; j0 < tile * 16 + 16; j0 += kBlocks * kRows) {
+            float4 lo[kBlocks], hi[kBlocks];
+            bool have[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int j = j0 + b * kRows;
+                const int32_t blk = block_of(p, w, j, entry_of(p, w, j));
+                have[b] = blk >= 0;
+                lo[b] = hi[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (have[b]) {
+                    lo[b] = *reinterpret_cast<const float4*>(bounds + blk * block_stride);
+                    hi[b] = *reinterpret_cast<const float4*>(bounds + blk * block_stride + D);
+                }
+            }
+            float v[kBlocks * G];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    v[b * G + i] = q[i].x * (q[i].x < 0.f ? lo[b].x : hi[b].x) + q[i].y * (q[i].y < 0.f ? lo[b].y : hi[b].y) +
+                                   (q[i].z * (q[i].z < 0.f ? lo[b].z : hi[b].z) + q[i].w * (q[i].w < 0.f ? lo[b].w : hi[b].w));
+            reduce_scatter<kBlocks * G, kLanes>(v);
+            // lane x holds heads of block x / (kLanes / kBlocks)
+            float best = v[0];
+            constexpr int kHeld = kBlocks * G > kLanes ? kBlocks * G / kLanes : 1;
+#pragma unroll
+            for (int i = 1; i < kHeld; ++i) best = max_nan(best, v[i]);
+#pragma unroll
+            for (int m = kLanes / kBlocks / 2; m; m >>= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, m));
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+                if (x == b * (kLanes / kBlocks) && have[b]) out[j0 + b * kRows] = best;
+        }
     }
 }
 
@@ -230,115 +372,290 @@ struct SelectParams {
     int* err;
 };
 
-// A score as an integer of the same order: NaN above +inf, -0 equal to +0,
-// everything below kForced.
-constexpr uint32_t kForced = 0xffffffffu;
+// A score as an integer of the same order: NaN above +inf, -0 equal to +0.  No
+// score gives 0, which marks what is not to be chosen from.
 __device__ __forceinline__ uint32_t score_key(float x) {
-    if (x != x) return kForced - 1;
+    if (x != x) return 0xffffffffu;
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 = +0
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelectThreads = 256;
-constexpr int kSelectWarps = kSelectThreads / 32;
+__device__ __forceinline__ int sum_lanes(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t min_lanes(uint32_t x) { return __reduce_min_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t max_lanes(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// One CTA per (row, kv head).  The K-th largest key is found digit by digit
-// (radix select: a histogram of 256 counts of the keys that still match the
-// digits found so far), then the blocks above it and the lowest-numbered
-// blocks equal to it are written in ascending order, their places from warp
-// ballots.  Counts are integers, so the order of the atomics changes nothing.
-__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const SelectParams p) {
-    __shared__ int hist[256];
-    __shared__ int warp_above[kSelectWarps], warp_equal[kSelectWarps];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_want;
+// The row of one (row, kv head) as the selection sees it.
+struct SelectRow {
+    const float* scores;
+    int32_t* out;
+    int blocks;      // of the row
+    int last;        // the first of its last num_last blocks
+    int num_first, want;  // want: blocks to choose besides the first and last
+    __device__ __forceinline__ bool always(int j) const { return j < num_first || j >= last; }
+    __device__ __forceinline__ uint32_t key(int j) const {
+        return j < blocks && !always(j) ? score_key(scores[j]) : 0u;
+    }
+};
+
+// False where the row is already written: no more blocks than max_selected
+// (all of them), or a bad length (none).  Called by `threads` threads.
+__device__ __forceinline__ bool select_row(const SelectParams& p, int64_t unit, int thread, int threads, SelectRow& r) {
+    const int64_t row = unit / p.num_kv_heads;
+    const int L = p.context_lens[row];
+    r.out = p.selected + unit * p.max_selected;
+    r.blocks = 0;
+    if (L < 0 || L > p.max_context_len) {
+        if (unit == row * p.num_kv_heads && thread == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+    } else {
+        r.blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
+    }
+    if (r.blocks <= p.max_selected) {
+        for (int i = thread; i < p.max_selected; i += threads) r.out[i] = i < r.blocks ? i : -1;
+        return false;
+    }
+    r.scores = p.scores + unit * p.score_stride;
+    r.num_first = p.num_first;
+    r.last = r.blocks - p.num_last;
+    r.want = p.max_selected - p.num_first - p.num_last;
+    return true;
+}
+
+// Short rows, at most 32 * kItems blocks: one warp a row, its keys in
+// registers.  The value of the last key to be taken is found by bisection, a
+// count over the warp a step, which ends early at any value that exactly
+// max_selected keys reach.
+constexpr int kShortItems = 8;
+
+__global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = blockIdx.x;
-    const int64_t row = unit / p.num_kv_heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int L = p.context_lens[row];
-    int32_t* out = p.selected + unit * p.max_selected;
-    int blocks = 0;
-    if (L < 0 || L > p.max_context_len) {
-        if (unit == row * p.num_kv_heads && tid == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-    } else {
-        blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
-    }
-    const int K = p.max_selected;
-    if (blocks <= K) {
-        for (int i = tid; i < K; i += kSelectThreads) out[i] = i < blocks ? i : -1;
-        return;
-    }
-    const float* scores = p.scores + unit * p.score_stride;
-    const int last = blocks - p.num_last;
-    auto key_of = [&](int j) { return j < p.num_first || j >= last ? kForced : score_key(scores[j]); };
-
-    // the K-th largest key: `prefix` holds the digits found, `want` how many of
-    // the keys that start with them are still to be taken
-    uint32_t prefix = 0, mask = 0;
-    int want = K;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < blocks; j += kSelectThreads) {
-            const uint32_t key = key_of(j);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int left = want, d = 255;
-            for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-            s_prefix = prefix | ((uint32_t)d << shift);
-            s_want = left;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        want = s_want;
-        mask |= 0xffu << shift;
-    }
-
-    // ascending output: `want` blocks equal to the threshold, and all above it
-    int done_above = 0, done_equal = 0;
-    for (int base = 0; base < blocks; base += kSelectThreads) {
-        const int j = base + tid;
-        const uint32_t key = j < blocks ? key_of(j) : 0;
-        const bool above = j < blocks && key > prefix, equal = j < blocks && key == prefix;
-        const unsigned ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
-        if (lane == 0) {
-            warp_above[warp] = __popc(ma);
-            warp_equal[warp] = __popc(me);
-        }
-        __syncthreads();
-        int a = done_above, e = done_equal;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= p.num_rows * p.num_kv_heads) return;
+    const int lane = threadIdx.x & 31;
+    SelectRow r;
+    if (!select_row(p, unit, lane, 32, r)) return;
+    uint32_t key[kShortItems], lo = 0xffffffffu, hi = 0;
 #pragma unroll
-        for (int w = 0; w < kSelectWarps; ++w) {
-            if (w < warp) {
-                a += warp_above[w];
-                e += warp_equal[w];
+    for (int i = 0; i < kShortItems; ++i) {
+        key[i] = r.key(32 * i + lane);
+        hi = max(hi, key[i]);
+        if (key[i]) lo = min(lo, key[i]);
+    }
+    lo = min_lanes(lo);
+    hi = max_lanes(hi);
+    // every key above hi is taken, none below lo; `want` of those in lo .. hi
+    int want = r.want;
+    if (want == 0) {
+        lo = hi = 0xffffffffu;
+    } else {
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kShortItems; ++i) n += key[i] >= mid && key[i] <= hi;
+            n = sum_lanes(n);
+            if (n == want) {
+                lo = mid;
+                break;
             }
-            done_above += warp_above[w];
-            done_equal += warp_equal[w];
+            if (n > want) {
+                lo = mid;
+            } else {
+                want -= n;
+                hi = mid - 1;
+            }
         }
-        const unsigned below = (1u << lane) - 1u;
-        a += __popc(ma & below);
-        e += __popc(me & below);
-        if (above || (equal && e < want)) out[a + min(e, want)] = j;
-        __syncthreads();
+    }
+    int at = 0;
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+    for (int i = 0; i < kShortItems; ++i) {
+        const int j = 32 * i + lane;
+        const unsigned edge = __ballot_sync(0xffffffffu, want > 0 && key[i] >= lo && key[i] <= hi);
+        const bool sure = (j < r.blocks && r.always(j)) || key[i] > hi;
+        const bool take = sure || ((edge >> lane & 1u) && __popc(edge & below) < want);
+        const unsigned taken = __ballot_sync(0xffffffffu, take);
+        if (take) r.out[at + __popc(taken & below)] = j;
+        at += __popc(taken);
+        want -= min(want, __popc(edge));
     }
 }
 
-template <typename T, int D>
-int launch_scores_d(const ScoreParams& p, cudaStream_t st) {
-    const int64_t grid = p.num_rows * p.num_kv_heads * p.tiles;
-    if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    const dim3 g((unsigned)grid), b(kWarps * 32);
-    switch (p.num_q_heads / p.num_kv_heads) {
-        case 1: return launch_pdl(block_scores_kernel<T, D, 1>, g, b, 0, st, p);
-        case 2: return launch_pdl(block_scores_kernel<T, D, 2>, g, b, 0, st, p);
-        case 4: return launch_pdl(block_scores_kernel<T, D, 4>, g, b, 0, st, p);
-        case 8: return launch_pdl(block_scores_kernel<T, D, 8>, g, b, 0, st, p);
-        case 16: return launch_pdl(block_scores_kernel<T, D, 16>, g, b, 0, st, p);
+// Long rows: one CTA a row.  The range of keys that holds the last one to be
+// taken is narrowed by histograms of kBins equal parts of it, until all of the
+// range is to be taken or it is one value; scores lie close together, so parts
+// of their own range tell them apart where the leading bits of a radix select
+// would all be the same (and the counters' atomics would collide).  Counts are
+// integers: the order of the atomics changes nothing.  Rows of up to THREADS *
+// kItems blocks are read once, longer ones once a pass.
+constexpr int kBins = 2048;
+constexpr int kItems = 8;
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_long_kernel(const SelectParams p) {
+    constexpr int kW = THREADS / 32;
+    constexpr int kOwn = kBins / THREADS;  // bins of one thread
+    __shared__ int hist[kBins];
+    __shared__ uint32_t s_lo[kW], s_hi[kW];
+    __shared__ int s_sum[kW], s_edge[kW];
+    __shared__ int s_bin, s_above, s_count;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    SelectRow r;
+    if (!select_row(p, blockIdx.x, tid, THREADS, r)) return;
+    const int chunks = (r.blocks + THREADS * kItems - 1) / (THREADS * kItems);
+    uint32_t key[kItems];
+    // warp w's part of a chunk is contiguous, item i its i-th 32 blocks
+    auto first_of = [&](int chunk) { return chunk * THREADS * kItems + warp * 32 * kItems + lane; };
+    auto load = [&](int chunk) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) key[i] = r.key(first_of(chunk) + 32 * i);
+    };
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) hist[tid * kOwn + i] = 0;
+    uint32_t lo = 0xffffffffu, hi = 0;
+    for (int c = 0; c < chunks; ++c) {
+        load(c);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            hi = max(hi, key[i]);
+            if (key[i]) lo = min(lo, key[i]);
+        }
+    }
+    lo = min_lanes(lo);
+    hi = max_lanes(hi);
+    if (lane == 0) {
+        s_lo[warp] = lo;
+        s_hi[warp] = hi;
+    }
+    __syncthreads();
+    lo = min_lanes(s_lo[lane % kW]);
+    hi = max_lanes(s_hi[lane % kW]);
+
+    // every key above hi is taken, none below lo; `want` of the `count` in lo .. hi
+    int want = r.want, count = r.blocks - p.num_first - p.num_last;
+    if (want == 0) lo = hi = 0xffffffffu;
+    while (want > 0 && want < count && lo < hi) {
+        const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift < kBins
+        for (int c = 0; c < chunks; ++c) {
+            if (chunks > 1) load(c);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                if (key[i] >= lo && key[i] <= hi) atomicAdd(&hist[(key[i] - lo) >> shift], 1);
+        }
+        __syncthreads();
+        // thread t owns bins top - t * kOwn and below; sums from the top
+        int own[kOwn], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int b = kBins - 1 - (tid * kOwn + i);
+            own[i] = hist[b];
+            hist[b] = 0;
+            sum += own[i];
+        }
+        int upto = sum;  // of this warp's threads up to this one
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += x;
+        }
+        if (lane == 31) s_sum[warp] = upto;
+        __syncthreads();
+        int above = upto - sum + sum_lanes(lane < warp ? s_sum[lane % kW] : 0);
+        if (above < want && above + sum >= want) {  // one thread
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                if (above < want && above + own[i] >= want) {
+                    s_bin = kBins - 1 - (tid * kOwn + i);
+                    s_above = above;
+                    s_count = own[i];
+                }
+                above += own[i];
+            }
+        }
+        __syncthreads();
+        want -= s_above;
+        count = s_count;
+        lo += (uint32_t)s_bin << shift;
+        hi = min(hi - lo, (1u << shift) - 1u) + lo;
+    }
+
+    // in ascending order: those surely taken, and the first `want` of lo .. hi
+    int done = 0, edges = 0;
+    const unsigned below = (1u << lane) - 1u;
+    for (int c = 0; c < chunks; ++c) {
+        if (chunks > 1) load(c);
+        unsigned sure[kItems], edge[kItems];
+        int n_sure = 0, n_edge = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int j = first_of(c) + 32 * i;
+            sure[i] = __ballot_sync(0xffffffffu, (j < r.blocks && r.always(j)) || key[i] > hi);
+            edge[i] = __ballot_sync(0xffffffffu, want > 0 && key[i] >= lo && key[i] <= hi);
+            n_sure += __popc(sure[i]);
+            n_edge += __popc(edge[i]);
+        }
+        __syncthreads();
+        if (lane == 0) {
+            s_sum[warp] = n_sure;
+            s_edge[warp] = n_edge;
+        }
+        __syncthreads();
+        const int all_sure = sum_lanes(lane < kW ? s_sum[lane] : 0), all_edge = sum_lanes(lane < kW ? s_edge[lane] : 0);
+        int a = done + sum_lanes(lane < warp ? s_sum[lane % kW] : 0);
+        int e = edges + sum_lanes(lane < warp ? s_edge[lane % kW] : 0);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const bool is_sure = sure[i] >> lane & 1u, is_edge = edge[i] >> lane & 1u;
+            const int rank = e + __popc(edge[i] & below);
+            if (is_sure || (is_edge && rank < want))
+                r.out[a + __popc(sure[i] & below) + min(rank, want)] = first_of(c) + 32 * i;
+            a += __popc(sure[i]);
+            e += __popc(edge[i]);
+        }
+        done += all_sure;
+        edges += all_edge;
+    }
+}
+
+template <int D, int NT>
+int launch_scores_mma(const ScoreParams& p, dim3 grid, cudaStream_t st) {
+    constexpr int kSmem = kWarps * 2 * 16 * 4 * D;
+    auto kernel = block_scores_mma_kernel<D, NT>;
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return PA_ERR_CUDA;
+        configured.fetch_or(bit);
+    }
+    return launch_pdl(kernel, grid, dim3(kWarps * 32), kSmem, st, p);
+}
+
+int launch_scores(ScoreParams p, int head_dim, int dtype, cudaStream_t st) {
+    // tiles of 16 blocks of one warp: one while the grid is short of 8 warps an
+    // SM, up to 8 once it is not
+    const int64_t units = p.num_rows * p.num_kv_heads;
+    const int64_t tiles = ((int64_t)p.max_context_len + 16 * p.block_size - 1) / (16 * p.block_size);
+    p.tiles_per_warp = (int)std::max((int64_t)1, std::min((int64_t)8, units * tiles / ((int64_t)num_sms() * 32)));
+    p.chunks = (int)((tiles + kWarps * p.tiles_per_warp - 1) / (kWarps * p.tiles_per_warp));
+    if (units > 0x7fffffff / p.chunks) return PA_ERR_UNSUPPORTED;
+    const dim3 g((unsigned)(units * p.chunks)), b(kWarps * 32);
+    const int group = p.num_q_heads / p.num_kv_heads;
+    if (dtype == PA_BF16) {
+        if (group == 16)
+            return head_dim == 128 ? launch_scores_mma<128, 2>(p, g, st) : launch_scores_mma<64, 2>(p, g, st);
+        return head_dim == 128 ? launch_scores_mma<128, 1>(p, g, st) : launch_scores_mma<64, 1>(p, g, st);
+    }
+    const bool wide = head_dim == 128;
+    switch (group) {
+        case 1: return launch_pdl(wide ? block_scores_f32_kernel<128, 1> : block_scores_f32_kernel<64, 1>, g, b, 0, st, p);
+        case 2: return launch_pdl(wide ? block_scores_f32_kernel<128, 2> : block_scores_f32_kernel<64, 2>, g, b, 0, st, p);
+        case 4: return launch_pdl(wide ? block_scores_f32_kernel<128, 4> : block_scores_f32_kernel<64, 4>, g, b, 0, st, p);
+        case 8: return launch_pdl(wide ? block_scores_f32_kernel<128, 8> : block_scores_f32_kernel<64, 8>, g, b, 0, st, p);
     }
     return PA_ERR_UNSUPPORTED;
 }
@@ -402,8 +719,8 @@ extern "C" int pa_block_scores(const void* q, const void* key_bounds, const int3
     if (!supported_head_dim(head_dim) || !supported_block_size(block_size) ||
         !supported_group(num_q_heads / num_kv_heads, dtype))
         return PA_ERR_UNSUPPORTED;
-    const int64_t tiles_of = ((int64_t)max_context_len + block_size - 1) / block_size;
-    if (max_context_len > (int64_t)max_blocks_per_seq * block_size || score_stride < tiles_of ||
+    const int64_t max_blocks = ((int64_t)max_context_len + block_size - 1) / block_size;
+    if (max_context_len > (int64_t)max_blocks_per_seq * block_size || score_stride < max_blocks ||
         (!seq_ids && num_rows > batch))
         return PA_ERR_INVALID_ARG;
     if (num_rows == 0 || max_context_len == 0) return PA_OK;
@@ -426,13 +743,9 @@ extern "C" int pa_block_scores(const void* q, const void* key_bounds, const int3
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
     p.num_blocks = num_blocks;
-    p.tiles = (int)((tiles_of + kWarps * kScoreBlocksPerWarp - 1) / (kWarps * kScoreBlocksPerWarp));
     p.err = error_word_ptr();
     if (!p.err) return PA_ERR_CUDA;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == PA_BF16)
-        return head_dim == 128 ? launch_scores_d<__nv_bfloat16, 128>(p, st) : launch_scores_d<__nv_bfloat16, 64>(p, st);
-    return head_dim == 128 ? launch_scores_d<float, 128>(p, st) : launch_scores_d<float, 64>(p, st);
+    return launch_scores(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pa_select_blocks(const float* scores, int64_t score_stride, const int32_t* context_lens,
@@ -462,6 +775,12 @@ extern "C" int pa_select_blocks(const float* scores, int64_t score_stride, const
     p.num_kv_heads = num_kv_heads;
     p.err = error_word_ptr();
     if (!p.err) return PA_ERR_CUDA;
-    return launch_pdl(select_blocks_kernel, dim3((unsigned)grid), dim3(kSelectThreads), 0,
-                      static_cast<cudaStream_t>(stream), p);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // by the longest row that may come: a warp a row while its keys fit the
+    // warp's registers, then a CTA of 256 threads, or of 1024
+    const int64_t blocks = ((int64_t)max_context_len + block_size - 1) / block_size;
+    if (blocks <= 32 * kShortItems)
+        return launch_pdl(select_short_kernel, dim3((unsigned)((grid + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, p);
+    if (blocks <= 256 * kItems) return launch_pdl(select_long_kernel<256>, dim3((unsigned)grid), dim3(256), 0, st, p);
+    return launch_pdl(select_long_kernel<1024>, dim3((unsigned)grid), dim3(1024), 0, st, p);
 }
