@@ -199,7 +199,7 @@ int pa_reshape_and_cache_decode(const void* key, const void* value, void* k_pool
  *                 itself when query_stride is num_q_heads * head_dim, and may
  *                 overlap no other argument
  *   slot_mapping  int64 [num_tokens]; negative = padding: nothing of the token
- *                 is read or written.  Slots must be distinct within one call.
+ *                 is written.  Slots must be distinct within one call.
  *   positions     int32 [num_axes][num_tokens], one position of each axis (one
  *                 axis for text; time, height and width for images and video)
  *   pair_axes     int32 [rotary_dim / 2], the axis each pair turns by, or NULL

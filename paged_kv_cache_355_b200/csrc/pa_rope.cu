@@ -10,14 +10,17 @@
 //
 // Bound by memory: each q row is read and written once, each k and v row read
 // once and written once; the arithmetic is about ten operations an element.
-// A row of D elements lies in D / 8 lanes (16 bytes each in bf16), so a warp
-// takes 2 (D 128) or 4 (D 64) heads at a time and the norm's sum and the far
-// half of a pair come by shuffles, without shared memory.  One warp stays with
-// one token, so that token's angles are loaded once for all of the warp's
-// heads.
+// A row of D elements lies in D / 8 lanes, so a warp takes 2 (D 128) or 4 (D 64)
+// heads at a time and the norm's sum comes by shuffles.  One warp stays with
+// one token (or a slice of its heads), whose angles it gathers once into shared
+// memory, and keeps the rows after the ones it works on in flight.  Where the
+// whole head is rotated in halves, a lane holds 4 elements of each half, so
+// both elements of a pair; in part rotated ones the far half comes by shuffles.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "pa.h"
 #include "pa_device.cuh"
@@ -28,7 +31,12 @@ namespace pa {
 namespace {
 
 constexpr int kRopeWarps = 4;
-constexpr int kUnroll = 4;  // head rows a lane has in flight
+
+enum Pairing {
+    kNeighbours,  // (2p, 2p + 1)
+    kHalves,      // (p, p + rotary_dim / 2)
+    kWholeHalves  // the same, rotary_dim = head_dim
+};
 
 struct RopeParams {
     const void *query, *key, *value;
@@ -52,70 +60,17 @@ struct RopeParams {
     int64_t num_tokens;
     int num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
-    int rows_per_warp;  // head rows (q, k and v counted) of one warp, a multiple of 32 / (D / 8)
-    int slices;         // warps of one token
+    int steps;   // of one warp; a step is 32 / (D / 8) head rows of q, k or v
+    int slices;  // warps of one token
     int* err;
 };
 
-// c and s of this lane's 8 elements, for the halves form one pair an element,
-// for the neighbours form one pair every two.  `chunk` is the lane's chunk of
-// the row; chunks at or past rotary_dim / 8 are not rotated.  Returns false
-// where a position or an axis is out of range (nothing is read there).
-template <bool INTERLEAVED>
-__device__ __forceinline__ bool load_angles(const RopeParams& p, int64_t token, int64_t text_pos, int chunk,
-                                            float (&c)[kChunk], float (&s)[kChunk]) {
-    const int half = p.rotary_dim / 2;
-    constexpr int kPairs = INTERLEAVED ? kChunk / 2 : kChunk;
-    if (chunk * kChunk >= p.rotary_dim) return true;
-    const int e = chunk * kChunk;
-    const int first = INTERLEAVED ? e / 2 : (e < half ? e : e - half);
-    float cc[kPairs], ss[kPairs];
-    if (p.pair_axes == nullptr) {
-        const int64_t pos = p.positions ? (int64_t)p.positions[token] : text_pos;
-        if (pos < 0 || pos >= p.max_position) return false;
-        const float* row = p.cos_sin + pos * p.rotary_dim + first;
-#pragma unroll
-        for (int i = 0; i < kPairs; i += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + i);
-            const float4 b = *reinterpret_cast<const float4*>(row + half + i);
-            cc[i] = a.x; cc[i + 1] = a.y; cc[i + 2] = a.z; cc[i + 3] = a.w;
-            ss[i] = b.x; ss[i + 1] = b.y; ss[i + 2] = b.z; ss[i + 3] = b.w;
-        }
-    } else {
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            const int axis = p.pair_axes[first + i];
-            int64_t pos = -1;
-            if (axis >= 0 && axis < p.num_axes) pos = p.positions[(int64_t)axis * p.num_tokens + token];
-            if (pos < 0 || pos >= p.max_position) {
-                ok = false;
-                continue;
-            }
-            const float* row = p.cos_sin + pos * p.rotary_dim + first + i;
-            cc[i] = row[0];
-            ss[i] = row[half];
-        }
-        if (!ok) return false;
-    }
-    // the second element of a pair takes +s, the first -s
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        if (INTERLEAVED) {
-            c[i] = cc[i / 2];
-            s[i] = (i & 1) ? ss[i / 2] : -ss[i / 2];
-        } else {
-            c[i] = cc[i];
-            s[i] = e < half ? -ss[i] : ss[i];
-        }
-    }
-    return true;
-}
-
-template <typename T, int D, bool INTERLEAVED, bool DECODE>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_cache_kernel(const RopeParams p) {
-    constexpr int kLanes = D / kChunk;    // lanes of one head row
-    constexpr int kHeads = 32 / kLanes;   // head rows of a warp at a time
+template <typename T, int D, Pairing PAIRING, bool DECODE>
+__global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const RopeParams p) {
+    constexpr int kLanes = D / kChunk;           // lanes of one head row
+    constexpr int kHeads = 32 / kLanes;          // head rows of a step
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // steps loaded together, 16 registers
+    __shared__ __align__(16) float angles[kRopeWarps][2][D / 2];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
@@ -123,11 +78,35 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_cache_kernel(const RopeP
     if (token >= p.num_tokens) return;  // whole warps
     const int slice = (int)(unit - token * p.slices);
     const int lane = threadIdx.x & 31;
-    const int sub = lane / kLanes, chunk = lane % kLanes;
+    const int sub = lane / kLanes, x = lane % kLanes;
+    // the lane's elements: 8 from `own`, or 4 there and 4 in the other half
+    const int own = PAIRING == kWholeHalves ? x * 4 : x * 8;
+    constexpr int kOther = PAIRING == kWholeHalves ? D / 2 : 4;
+
+    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
+    const int q_steps = (Hq + kHeads - 1) / kHeads, kv_steps = (Hkv + kHeads - 1) / kHeads;
+    const int first = slice * p.steps, end = min(first + p.steps, q_steps + 2 * kv_steps);
+    const T* q_src = static_cast<const T*>(p.query) + token * p.q_stride + own;
+    const T* k_src = static_cast<const T*>(p.key) + token * p.k_stride + own;
+    const T* v_src = static_cast<const T*>(p.value) + token * p.v_stride + own;
+    Chunk<T> rows[kAhead];
+    auto load = [&](Chunk<T>(&to)[kAhead], int from) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = from + u;  // the same for every lane
+            const T* src = s < q_steps ? q_src : s < q_steps + kv_steps ? k_src : v_src;
+            const int head = (s < q_steps ? s : s < q_steps + kv_steps ? s - q_steps : s - q_steps - kv_steps) * kHeads + sub;
+            to[u] = Chunk<T>{};
+            if (s < end && head < (s < q_steps ? Hq : Hkv)) to[u].load(src + (int64_t)head * D, src + (int64_t)head * D + kOther);
+        }
+    };
+    load(rows, first);  // beside the look-up of where they go
+    Chunk<T> wq{}, wk{};
+    if (p.q_weight) wq.load(static_cast<const T*>(p.q_weight) + own, static_cast<const T*>(p.q_weight) + own + kOther);
+    if (p.k_weight) wk.load(static_cast<const T*>(p.k_weight) + own, static_cast<const T*>(p.k_weight) + own + kOther);
 
     // where the token goes
-    int64_t slot = -1;
-    int64_t text_pos = -1;
+    int64_t slot = -1, text_pos = -1;
     bool bad = false;
     if (DECODE) {
         const int L = p.context_lens[token];
@@ -143,116 +122,129 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_cache_kernel(const RopeP
         slot = p.slot_mapping[token];
         bad = slot >= p.num_blocks * p.block_size;
     }
-    float c[kChunk], s[kChunk];
-    if (slot >= 0 && !bad) bad = !load_angles<INTERLEAVED>(p, token, text_pos, chunk, c, s);
-    bad = __any_sync(0xffffffffu, bad);
+    // its angles, a pair or two a lane; a bad position or axis reads nothing
+    const int half = p.rotary_dim / 2;
+    float(*cs)[D / 2] = angles[threadIdx.x >> 5];
+    if (DECODE ? text_pos >= 0 : slot >= 0) {
+#pragma unroll
+        for (int i = 0; i < D / 2; i += 32) {
+            const int pair = i + lane;
+            if (pair >= half) break;
+            const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
+            int64_t pos = text_pos;
+            if (p.positions) pos = axis >= 0 && axis < p.num_axes ? (int64_t)p.positions[(int64_t)axis * p.num_tokens + token] : -1;
+            if (pos >= 0 && pos < p.max_position) {
+                cs[0][pair] = p.cos_sin[pos * p.rotary_dim + pair];
+                cs[1][pair] = p.cos_sin[pos * p.rotary_dim + half + pair];
+            } else {
+                bad = true;
+            }
+        }
+    }
+    bad = __any_sync(0xffffffffu, bad);  // and the angles are in for every lane
     const bool write = slot >= 0 && !bad;
     if (slice == 0 && lane == 0) {
         if (bad) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
         if (p.slots_out) p.slots_out[token] = write ? slot : -1;
     }
     if (!write) return;  // the same for every lane
+    __syncwarp();
 
-    const bool turned = chunk * kChunk < p.rotary_dim;
-    const int shift = p.rotary_dim / (2 * kChunk);  // chunks between the halves of a pair
-    const int partner = !turned ? lane : (chunk < shift ? lane + shift : lane - shift);
+    // cosine and sine of the lane's pairs
+    constexpr int kPairs = PAIRING == kHalves ? 8 : 4;
+    const bool turned = PAIRING == kWholeHalves || x * kChunk < p.rotary_dim;
+    const int shift = p.rotary_dim / (2 * kChunk);  // kHalves: lanes between the elements of a pair
+    const bool second = PAIRING == kHalves && x >= shift;
+    const int partner = !turned ? lane : second ? lane - shift : lane + shift;
+    float c[kPairs], s[kPairs];
+    {
+        const int at = PAIRING == kHalves ? (second ? x - shift : x) * 8 : x * 4;
+#pragma unroll
+        for (int i = 0; i < kPairs; i += 4) {
+            const float4 a = turned ? *reinterpret_cast<const float4*>(&cs[0][at + i]) : float4{};
+            const float4 b = turned ? *reinterpret_cast<const float4*>(&cs[1][at + i]) : float4{};
+            c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+            s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
+        }
+    }
     const int64_t blk = slot / p.block_size;
     const int off = (int)(slot - blk * p.block_size);
-    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
-    const int total = Hq + 2 * Hkv;
-    const int row_end = min(total, (slice + 1) * p.rows_per_warp);
-
-    float wq[kChunk], wk[kChunk];
-    if (p.q_weight) {
-        Chunk<T> w;
-        w.load(static_cast<const T*>(p.q_weight) + chunk * kChunk);
-        w.to_f32(wq);
-    }
-    if (p.k_weight) {
-        Chunk<T> w;
-        w.load(static_cast<const T*>(p.k_weight) + chunk * kChunk);
-        w.to_f32(wk);
-    }
-    const T* q_row = static_cast<const T*>(p.query) + token * p.q_stride + chunk * kChunk;
-    const T* k_row = static_cast<const T*>(p.key) + token * p.k_stride + chunk * kChunk;
-    const T* v_row = static_cast<const T*>(p.value) + token * p.v_stride + chunk * kChunk;
-    T* q_dst = static_cast<T*>(p.query_out) + token * Hq * D + chunk * kChunk;
-    const int64_t pool_row = ((blk * Hkv) * p.block_size + off) * D + chunk * kChunk;  // kv head 0
+    T* q_dst = static_cast<T*>(p.query_out) + token * Hq * D + own;
+    const int64_t pool_row = ((blk * Hkv) * p.block_size + off) * D + own;  // kv head 0
     T* k_dst = static_cast<T*>(p.k_pool) + pool_row;
     T* v_dst = static_cast<T*>(p.v_pool) + pool_row;
     const int64_t head_stride = (int64_t)p.block_size * D;  // between kv heads in the pool
 
-    for (int base = slice * p.rows_per_warp; base < row_end; base += kHeads * kUnroll) {
-        Chunk<T> raw[kUnroll];
+    for (int from = first; from < end; from += kAhead) {
+        Chunk<T> next[kAhead];
+        if (from + kAhead < end) load(next, from + kAhead);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = base + u * kHeads + sub;
-            if (r < row_end) {
-                const T* src = r < Hq ? q_row + (int64_t)r * D
-                                      : (r < Hq + Hkv ? k_row + (int64_t)(r - Hq) * D
-                                                      : v_row + (int64_t)(r - Hq - Hkv) * D);
-                raw[u].load(src);
-            } else {
-                raw[u] = Chunk<T>{};
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = base + u * kHeads + sub;
-            if (base + u * kHeads >= row_end) break;  // the same for every lane
-            if (base + u * kHeads < Hq + Hkv) {       // at least one q or k row
-                float x[kChunk];
-                raw[u].to_f32(x);
-                const bool is_q = r < Hq;
+        for (int u = 0; u < kAhead; ++u) {
+            const int st = from + u;
+            if (st >= end) break;
+            const bool is_q = st < q_steps, is_v = st >= q_steps + kv_steps;
+            if (!is_v) {
+                float y[kChunk];
+                rows[u].to_f32(y);
                 if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
                     float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) sum = fmaf(x[i], x[i], sum);
-                    // rows of one warp may differ in whether they have a norm,
-                    // the lanes of one row do not
-                    const unsigned row_mask = (kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << (sub * kLanes));
+                    for (int i = 0; i < kChunk; ++i) sum = fmaf(y[i], y[i], sum);
 #pragma unroll
-                    for (int m = kLanes / 2; m; m >>= 1) sum += __shfl_xor_sync(row_mask, sum, m);
+                    for (int m = kLanes / 2; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                     const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
+                    float w[kChunk];
+                    (is_q ? wq : wk).to_f32(w);
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) x[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
+                    for (int i = 0; i < kChunk; ++i) y[i] = y[i] * inv * w[i];
                 }
-                float y[kChunk];
+                if (PAIRING == kHalves) {
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i)
-                    y[i] = INTERLEAVED ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], partner);
-                if (r < Hq + Hkv) {
-                    if (turned) {
-#pragma unroll
-                        for (int i = 0; i < kChunk; ++i) x[i] = fmaf(x[i], c[i], y[i] * s[i]);
+                    for (int i = 0; i < kChunk; ++i) {
+                        const float z = __shfl_sync(0xffffffffu, y[i], partner);
+                        if (turned) y[i] = fmaf(y[i], c[i % kPairs], second ? z * s[i % kPairs] : -(z * s[i % kPairs]));
                     }
-                    raw[u].from_f32(x);
+                } else if (turned) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int a = PAIRING == kWholeHalves ? i : 2 * i, b = PAIRING == kWholeHalves ? i + 4 : 2 * i + 1;
+                        const float y1 = y[a], y2 = y[b];
+                        y[a] = fmaf(y1, c[i], -(y2 * s[i]));
+                        y[b] = fmaf(y2, c[i], y1 * s[i]);
+                    }
                 }
+                rows[u].from_f32(y);
             }
-            if (r < row_end) {
-                T* dst = r < Hq ? q_dst + (int64_t)r * D
-                                : (r < Hq + Hkv ? k_dst + (r - Hq) * head_stride : v_dst + (r - Hq - Hkv) * head_stride);
-                raw[u].store(dst);
-            }
+            const int head = (is_q ? st : is_v ? st - q_steps - kv_steps : st - q_steps) * kHeads + sub;
+            T* dst = is_q ? q_dst + (int64_t)head * D : (is_v ? v_dst : k_dst) + head * head_stride;
+            if (head < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + kOther);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) rows[u] = next[u];
     }
 }
 
 template <typename T, int D, bool DECODE>
 int launch_rope(RopeParams p, bool interleaved, cudaStream_t stream) {
     constexpr int kHeads = 32 / (D / kChunk);
-    const int total = p.num_q_heads + 2 * p.num_kv_heads;
-    // head rows of one warp: as few as one step of the warp while the grid is
-    // short of 32 warps an SM, as many as 4 unrolled steps once it is not
-    const int64_t steps = ((int64_t)total + kHeads - 1) / kHeads;
-    int64_t per_warp = steps * p.num_tokens / ((int64_t)num_sms() * 32);
-    if (per_warp < 1) per_warp = 1;
-    if (per_warp > 4 * kUnroll) per_warp = 4 * kUnroll;
-    p.rows_per_warp = (int)per_warp * kHeads;
-    p.slices = (total + p.rows_per_warp - 1) / p.rows_per_warp;
+    const int64_t steps = (p.num_q_heads + kHeads - 1) / kHeads + 2 * ((p.num_kv_heads + kHeads - 1) / kHeads);
+    // Steps of one warp.  A token's look-ups are paid once a warp, so few tokens
+    // share out their heads (4 tokens of 12 heads: 2.1 us with one step a warp,
+    // 2.5 with all three), but not beyond one load of several steps where that
+    // fills the SMs (256 tokens of 24 steps: 5.8 us with one, 3.9 with four);
+    // many take a whole token a warp (24k tokens of 40 steps: 187 us with 24
+    // steps, 164 with 40) as long as that leaves 64 warps an SM to even out.
+    const int64_t all = steps * p.num_tokens, sms = num_sms();
+    int64_t per_warp = all / (sms * 64);
+    if (per_warp < 4 && all >= sms * 32) per_warp = 4;
+    per_warp = std::max((int64_t)1, std::min(per_warp, steps));
+    p.slices = (int)((steps + per_warp - 1) / per_warp);
+    p.steps = (int)((steps + p.slices - 1) / p.slices);  // evened out
     const int64_t blocks = (p.num_tokens * p.slices + kRopeWarps - 1) / kRopeWarps;
     if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    auto kernel = interleaved ? rope_cache_kernel<T, D, true, DECODE> : rope_cache_kernel<T, D, false, DECODE>;
+    auto kernel = interleaved            ? rope_cache_kernel<T, D, kNeighbours, DECODE>
+                  : p.rotary_dim == D    ? rope_cache_kernel<T, D, kWholeHalves, DECODE>
+                                         : rope_cache_kernel<T, D, kHalves, DECODE>;
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRopeWarps * 32), 0, stream, p);
 }
 

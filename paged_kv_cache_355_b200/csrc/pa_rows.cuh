@@ -22,6 +22,15 @@ struct Chunk<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+    // elements 0..3 at p, 4..7 at q
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(q);
+        a = make_uint4(x.x, x.y, y.x, y.y);
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, __nv_bfloat16* q) const {
+        *reinterpret_cast<uint2*>(p) = make_uint2(a.x, a.y);
+        *reinterpret_cast<uint2*>(q) = make_uint2(a.z, a.w);
+    }
     __device__ __forceinline__ void to_f32(float (&x)[kChunk]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -41,13 +50,15 @@ struct Chunk<__nv_bfloat16> {
 template <>
 struct Chunk<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
+    __device__ __forceinline__ void load(const float* p) { load(p, p + 4); }
+    __device__ __forceinline__ void store(float* p) const { store(p, p + 4); }
+    __device__ __forceinline__ void load(const float* p, const float* q) {
         a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + 4);
+        b = *reinterpret_cast<const float4*>(q);
     }
-    __device__ __forceinline__ void store(float* p) const {
+    __device__ __forceinline__ void store(float* p, float* q) const {
         *reinterpret_cast<float4*>(p) = a;
-        *reinterpret_cast<float4*>(p + 4) = b;
+        *reinterpret_cast<float4*>(q) = b;
     }
     __device__ __forceinline__ void to_f32(float (&x)[kChunk]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
