@@ -38,85 +38,218 @@ struct BoundsParams {
     int max_query_len, batch, num_kv_heads, block_size;
     int64_t num_blocks;
     int max_touched;  // blocks that max_query_len new tokens can lie in
+    int heads_per_warp;
     int* err;
 };
 
-// One warp per (sequence, block with new tokens, kv head): it reads the rows
-// of the block's tokens, 32 / (D / 8) rows at a time, keeps the running
-// minimum and maximum of its 8 channels, and joins the rows' lanes by
-// shuffles.  Bound by the read of the keys: one pass, D * 2 values written for
-// block_size * D read.  The whole block is read again for every new token
-// rather than its bounds updated, so that the call can be repeated and follows
-// a copied or rewritten block.
-template <typename T, int D>
+// The running minimum and maximum of a lane's 8 channels, NaN kept.
+template <typename T>
+struct Range;
+
+__device__ __forceinline__ uint32_t min2_nan(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
+template <>
+struct Range<__nv_bfloat16> {
+    uint32_t lo[4], hi[4];  // pairs of channels
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = 0x7f807f80u;  // +inf
+            hi[i] = 0xff80ff80u;
+        }
+    }
+    __device__ __forceinline__ void take(const Chunk<__nv_bfloat16>& c) {
+        const uint32_t x[4] = {c.a.x, c.a.y, c.a.z, c.a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = min2_nan(lo[i], x[i]);
+            hi[i] = max2_nan(hi[i], x[i]);
+        }
+    }
+    __device__ __forceinline__ void join(int lanes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = min2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], lanes));
+            hi[i] = max2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], lanes));
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, bool high) const {
+        *reinterpret_cast<uint4*>(p) =
+            high ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+};
+
+template <>
+struct Range<float> {
+    float lo[8], hi[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __int_as_float(0x7f800000);
+            hi[i] = __int_as_float(0xff800000);
+        }
+    }
+    __device__ __forceinline__ void take(const Chunk<float>& c) {
+        float x[kChunk];
+        c.to_f32(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = min_nan(lo[i], x[i]);
+            hi[i] = max_nan(hi[i], x[i]);
+        }
+    }
+    __device__ __forceinline__ void join(int lanes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], lanes));
+            hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], lanes));
+        }
+    }
+    __device__ __forceinline__ void store(float* p, bool high) const {
+        Chunk<float> c;
+        float x[kChunk];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = high ? hi[i] : lo[i];
+        c.from_f32(x);
+        c.store(p);
+    }
+};
+
+// One warp per (sequence, block with new tokens, part of the kv heads): it takes
+// the rows of the block's tokens head by head, through a ring of four pieces of
+// 4 KB that asynchronous copies fill, and joins the lanes' ranges by shuffles.
+// Bound by the read of the keys: one pass, 2 D values written for BS * D read;
+// a lane reads back only what it copied itself, so no barrier is needed.  The
+// whole block is read again for every new token rather than its bounds updated,
+// so that the call can be repeated and follows a copied or rewritten block.
+constexpr int kPieces = 4;
+constexpr int kPieceBytes = 4096;
+
+template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsParams p) {
     constexpr int kLanes = D / kChunk;
-    constexpr int kRows = 32 / kLanes;
+    constexpr int kRows = 32 / kLanes;                        // rows side by side
+    constexpr int kOwn = BS / kRows;                          // rows of one lane
+    constexpr int kMost = kPieceBytes / (32 * kChunk * (int)sizeof(T));  // of a piece
+    constexpr int kBatch = kOwn < kMost ? kOwn : kMost;
+    constexpr int kPerHead = kOwn / kBatch;                   // pieces of one head
+    constexpr int kVec = kChunk * sizeof(T) / 16;             // 16-byte vectors of a chunk
+    extern __shared__ __align__(16) uint8_t ring[];           // [warp][piece][row][vector][lane]
     griddep_wait();
     griddep_launch_dependents();
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t per_seq = (int64_t)p.max_touched * p.num_kv_heads;
+    const int parts = (p.num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp;
+    const int64_t per_seq = (int64_t)p.max_touched * parts;
     const int64_t b = unit / per_seq;
     if (b >= p.batch) return;
     const int64_t rem = unit - b * per_seq;
-    const int i = (int)(rem / p.num_kv_heads);
-    const int h = (int)(rem - (int64_t)i * p.num_kv_heads);
+    const int i = (int)(rem / parts);
+    const int part = (int)(rem - (int64_t)i * parts);
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, chunk = lane % kLanes;
 
     const int L = p.context_lens[b];
     int64_t n = L > 0 ? 1 : 0;
     if (p.query_start) n = (int64_t)p.query_start[b + 1] - p.query_start[b];
-    if (L < 0 || n < 0 || n > L || n > p.max_query_len || L > (int64_t)p.max_blocks_per_seq * p.block_size) {
+    if (L < 0 || n < 0 || n > L || n > p.max_query_len || L > (int64_t)p.max_blocks_per_seq * BS) {
         if (rem == 0 && lane == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
         return;
     }
     if (n == 0) return;
-    const int64_t j = (L - n) / p.block_size + i;
-    if (j > (L - 1) / p.block_size) return;
+    const int64_t j = (L - n) / BS + i;
+    if (j > (L - 1) / BS) return;
     const int64_t blk = p.block_tables[b * p.max_blocks_per_seq + j];
     if (blk < 0 || blk >= p.num_blocks) {
-        if (h == 0 && lane == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+        if (part == 0 && lane == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
         return;
     }
-    const int64_t left = L - j * p.block_size;
-    const int held = left < p.block_size ? (int)left : p.block_size;  // tokens of the block
-    const T* src = static_cast<const T*>(p.k_pool) + ((blk * p.num_kv_heads + h) * p.block_size) * D + chunk * kChunk;
+    const int64_t left = L - j * BS;
+    const int held = left < BS ? (int)left : BS;  // tokens of the block
+    const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, p.num_kv_heads);
+    const int64_t row = blk * p.num_kv_heads + h0;
+    const T* src = static_cast<const T*>(p.k_pool) + row * (BS * D) + sub * D + chunk * kChunk;
+    T* dst = static_cast<T*>(p.key_bounds) + row * (2 * D) + (sub & 1) * D + chunk * kChunk;
+    uint8_t* mine = ring + (threadIdx.x >> 5) * (kPieces * kPieceBytes) + lane * 16;
 
-    float lo[kChunk], hi[kChunk];
+    const int pieces = (h1 - h0) * kPerHead;
+    int fetched = 0;
+    auto fetch = [&]() {
+        if (fetched < pieces) {
+            const int t0 = fetched % kPerHead * kBatch;
+            const uint32_t to = smem_addr(mine) + fetched % kPieces * kPieceBytes;
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-        lo[e] = __int_as_float(0x7f800000);
-        hi[e] = __int_as_float(0xff800000);
-    }
-#pragma unroll 4
-    for (int t = sub; t < held; t += kRows) {
-        Chunk<T> raw;
-        raw.load(src + t * D);
-        float x[kChunk];
-        raw.to_f32(x);
+            for (int t = 0; t < kBatch; ++t)
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            lo[e] = min_nan(lo[e], x[e]);
-            hi[e] = max_nan(hi[e], x[e]);
+                for (int v = 0; v < kVec; ++v)
+                    copy_async16(to + (t * kVec + v) * 512, src + (t0 + t) * kRows * D + v * (16 / sizeof(T)),
+                                 (t0 + t) * kRows + sub < held);
+            ++fetched;
+            if (fetched % kPerHead == 0) src += BS * D;
+        }
+        copy_async_commit();
+    };
+#pragma unroll
+    for (int f = 0; f < kPieces; ++f) fetch();
+    Range<T> r;
+    for (int done = 0; done < pieces; ++done) {
+        copy_async_wait<kPieces - 1>();
+        if (kPerHead == 1 || done % kPerHead == 0) r.clear();
+        const int t0 = done % kPerHead * kBatch;
+        const uint8_t* from = mine + done % kPieces * kPieceBytes;
+        Chunk<T> rows[kBatch];
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+            rows[t].load(reinterpret_cast<const T*>(from + t * kVec * 512),
+                         reinterpret_cast<const T*>(from + t * kVec * 512 + (kVec == 2 ? 512 : 8)));
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+            if ((t0 + t) * kRows + sub < held) r.take(rows[t]);
+        fetch();
+        if (kPerHead == 1 || (done + 1) % kPerHead == 0) {
+#pragma unroll
+            for (int m = kLanes; m < 32; m <<= 1) r.join(m);
+            if (sub < 2) r.store(dst, sub == 1);
+            dst += 2 * D;
         }
     }
-#pragma unroll
-    for (int m = kLanes; m < 32; m <<= 1) {
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            lo[e] = min_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], m));
-            hi[e] = max_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], m));
-        }
+    copy_async_wait<0>();
+}
+
+template <typename T, int D>
+int launch_bounds(BoundsParams p, cudaStream_t st) {
+    constexpr int kSmem = kWarps * kPieces * kPieceBytes;
+    // a warp takes as many kv heads of a block as leave 64 warps an SM
+    const int64_t all = (int64_t)p.batch * p.max_touched * p.num_kv_heads;
+    const int64_t heads = std::max((int64_t)1, std::min((int64_t)p.num_kv_heads, all / ((int64_t)num_sms() * 64)));
+    const int64_t parts = (p.num_kv_heads + heads - 1) / heads;
+    p.heads_per_warp = (int)((p.num_kv_heads + parts - 1) / parts);
+    const int64_t blocks = ((int64_t)p.batch * p.max_touched * parts + kWarps - 1) / kWarps;
+    if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    auto kernel = p.block_size == 8    ? key_bounds_kernel<T, D, 8>
+                  : p.block_size == 16 ? key_bounds_kernel<T, D, 16>
+                                       : key_bounds_kernel<T, D, 32>;
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        const void* const kernels[] = {(const void*)key_bounds_kernel<T, D, 8>, (const void*)key_bounds_kernel<T, D, 16>,
+                                       (const void*)key_bounds_kernel<T, D, 32>};
+        for (const void* k : kernels)
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+                return PA_ERR_CUDA;
+        configured.fetch_or(bit);
     }
-    if (sub == 0) {
-        T* dst = static_cast<T*>(p.key_bounds) + ((blk * p.num_kv_heads + h) * 2) * D + chunk * kChunk;
-        Chunk<T> out;
-        out.from_f32(lo);
-        out.store(dst);
-        out.from_f32(hi);
-        out.store(dst + D);
-    }
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), kSmem, st, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -692,18 +825,12 @@ extern "C" int pa_update_key_bounds(const void* k_pool, void* key_bounds, const 
     // n tokens that end anywhere lie in at most (n - 2) / bs + 2 blocks
     p.max_touched = (int)(((int64_t)p.max_query_len + block_size - 2) / block_size) + 1;
     if (p.max_touched > max_blocks_per_seq) p.max_touched = max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
-    const int64_t units = (int64_t)batch * p.max_touched * num_kv_heads;
-    const int64_t blocks = (units + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     p.err = error_word_ptr();
     if (!p.err) return PA_ERR_CUDA;
-    const dim3 g((unsigned)blocks), b(kWarps * 32);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == PA_BF16)
-        return head_dim == 128 ? launch_pdl(key_bounds_kernel<__nv_bfloat16, 128>, g, b, 0, st, p)
-                               : launch_pdl(key_bounds_kernel<__nv_bfloat16, 64>, g, b, 0, st, p);
-    return head_dim == 128 ? launch_pdl(key_bounds_kernel<float, 128>, g, b, 0, st, p)
-                           : launch_pdl(key_bounds_kernel<float, 64>, g, b, 0, st, p);
+        return head_dim == 128 ? launch_bounds<__nv_bfloat16, 128>(p, st) : launch_bounds<__nv_bfloat16, 64>(p, st);
+    return head_dim == 128 ? launch_bounds<float, 128>(p, st) : launch_bounds<float, 64>(p, st);
 }
 
 extern "C" int pa_block_scores(const void* q, const void* key_bounds, const int32_t* block_tables,
