@@ -31,7 +31,8 @@ def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
 
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)
+        return value
     raise AttributeError(name)
 
 
@@ -80,16 +81,18 @@ def sparse_decode_step(query, key, value, k_pool, v_pool, key_bounds, block_tabl
     """
     from . import _binding as b
 
-    with b._device_guard(stream, query, k_pool, v_pool, cow_pairs):
-        if cow_pairs is not None and cow_pairs.numel():
+    bs = k_pool.shape[2]
+    if cow_pairs is not None and cow_pairs.numel():
+        import torch
+
+        with torch.cuda.device(k_pool.device):
             b.pa_copy_blocks(k_pool, v_pool, cow_pairs, stream=stream)
-        b.pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, cos_sin,
-                                   positions=positions, pair_axes=pair_axes, interleaved=interleaved, q_weight=q_weight,
-                                   k_weight=k_weight, eps=eps, slot_mapping=slots, stream=stream)
-        b.pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, stream=stream)
-        b.pa_block_scores(query_out, key_bounds, block_tables, context_lens, max_context_len, k_pool.shape[2], scores,
-                          stream=stream)
-        b.pa_select_blocks(scores, context_lens, max_context_len, k_pool.shape[2], selected, num_first=num_first,
-                           num_last=num_last, stream=stream)
-        b.pa_paged_attention_decode_sparse(query_out, k_pool, v_pool, block_tables, context_lens, selected, scale, out,
-                                           stream=stream)
+    b.pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, cos_sin,
+                               positions=positions, pair_axes=pair_axes, interleaved=interleaved, q_weight=q_weight,
+                               k_weight=k_weight, eps=eps, slot_mapping=slots, stream=stream)
+    b.pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, stream=stream)
+    b.pa_block_scores(query_out, key_bounds, block_tables, context_lens, max_context_len, bs, scores, stream=stream)
+    b.pa_select_blocks(scores, context_lens, max_context_len, bs, selected, num_first=num_first, num_last=num_last,
+                       stream=stream)
+    b.pa_paged_attention_decode_sparse(query_out, k_pool, v_pool, block_tables, context_lens, selected, scale, out,
+                                       stream=stream)

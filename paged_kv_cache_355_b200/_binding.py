@@ -10,7 +10,6 @@ this module fails.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -412,72 +411,92 @@ def pa_paged_attention_prefill(q, k_pool, v_pool, block_tables, context_lens, qu
 
 
 # The calls below take the device from their tensors: they run on it whichever
-# device is current, and refuse tensors of different devices.
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _device_guard(stream, first: torch.Tensor, *others):
-    device = first.device
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors lie on different devices: {device} and {t.device}")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return _NO_GUARD  # a tensor that is not on a GPU is refused by name
-    return torch.cuda.device(device)
-
-
-def _opt(t, name: str, dtype=None):
-    return None if t is None else _dev(t, name, dtype)
-
-
-def _token_rows(t, name: str, shape, dtype) -> tuple[int, int]:
-    """Pointer and token stride of [tokens, heads, head_dim] rows whose tokens
-    may lie apart (a slice of one projection's output)."""
+# device is current, and refuse tensors of different devices.  They are short on
+# the device, so what they do on the host is kept short too: one test of each
+# tensor, and the stream handle without a Stream object around it.
+def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    return t.get_device()
+
+
+def _on(t, name: str, dtype, device: int) -> int:
+    """Pointer of a contiguous tensor of this type on this device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, dtype, device)
+    return t.data_ptr()
+
+
+def _refuse(t, name: str, dtype, device: int) -> None:
+    _dev(t, name, dtype)
+    raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
+
+
+def _opt(t, name: str, dtype, device: int):
+    return None if t is None else _on(t, name, dtype, device)
+
+
+def _call(name: str, device: int, stream, *args) -> None:
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if device == torch.cuda.current_device():
+        status = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_lib, name)(*args, raw)
+    if status != 0:
+        raise PAError(name, status)
+
+
+def _token_rows(t, name: str, T: int, H: int, D: int, dtype, device: int) -> tuple[int, int]:
+    """Pointer and token stride of [tokens, heads, head_dim] rows whose tokens
+    may lie apart (a slice of one projection's output)."""
+    if _device_of(t, name) != device:
+        raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    T, H, D = shape
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
     st = t.stride()
     if st[2] != 1 or (H > 1 and st[1] != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return t.data_ptr(), (st[0] if T > 1 else H * D)
 
 
-def _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, q_weight, k_weight):
-    """Checks that both rotary calls share; returns (T, Hq, Hkv, D, NB, bs, dtype
-    code, row arguments, position arguments, weight arguments)."""
+def _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, interleaved, q_weight,
+               k_weight, eps):
+    """Checks that both rotary calls share; returns the device, the sizes that
+    end the argument list, the arguments before the slots and those after."""
     T, Hq, D = query.shape
     NB, Hkv, bs, D2 = k_pool.shape
+    dtype = query.dtype
     dt = _kv_dtype(query)
-    if D2 != D or v_pool.shape != k_pool.shape or tuple(query_out.shape) != (T, Hq, D):
+    if D2 != D or v_pool.shape != k_pool.shape or query_out.shape != query.shape:
         raise ValueError("query / query_out / pool shapes disagree")
-    qp, qs = _token_rows(query, "query", (T, Hq, D), query.dtype)
-    kp, ks = _token_rows(key, "key", (T, Hkv, D), query.dtype)
-    vp, vs = _token_rows(value, "value", (T, Hkv, D), query.dtype)
+    device = _device_of(query, "query")
+    qp, qs = _token_rows(query, "query", T, Hq, D, dtype, device)
+    kp, ks = _token_rows(key, "key", T, Hkv, D, dtype, device)
+    vp, vs = _token_rows(value, "value", T, Hkv, D, dtype, device)
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
     max_position, rotary_dim = cos_sin.shape
     axes = 1
     if positions is not None:
-        if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        dims = positions.dim()
+        if dims not in (1, 2) or positions.shape[-1] != T:
             raise ValueError("positions must be [tokens] or [axes, tokens]")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        axes = 1 if dims == 1 else positions.shape[0]
     if pair_axes is not None and pair_axes.numel() != rotary_dim // 2:
         raise ValueError("pair_axes needs rotary_dim / 2 entries")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.numel() != D:
-            raise ValueError(f"{name} needs head_dim entries")
-    rows = (qp, kp, vp, qs, ks, vs, _dev(query_out, "query_out", query.dtype), _dev(k_pool, "k_pool", query.dtype),
-            _dev(v_pool, "v_pool", query.dtype))
-    pos = (_opt(positions, "positions", torch.int32), axes, _opt(pair_axes, "pair_axes", torch.int32),
-           _dev(cos_sin, "cos_sin", torch.float32), max_position, rotary_dim)
-    weights = (_opt(q_weight, "q_weight", query.dtype), _opt(k_weight, "k_weight", query.dtype))
-    return T, Hq, Hkv, D, NB, bs, dt, rows, pos, weights
+    if (q_weight is not None and q_weight.numel() != D) or (k_weight is not None and k_weight.numel() != D):
+        raise ValueError("q_weight and k_weight need head_dim entries")
+    rows = (qp, kp, vp, qs, ks, vs, _on(query_out, "query_out", dtype, device), _on(k_pool, "k_pool", dtype, device),
+            _on(v_pool, "v_pool", dtype, device))
+    turn = (_opt(positions, "positions", torch.int32, device), axes, _opt(pair_axes, "pair_axes", torch.int32, device),
+            _on(cos_sin, "cos_sin", torch.float32, device), max_position, rotary_dim, 1 if interleaved else 0,
+            _opt(q_weight, "q_weight", dtype, device), _opt(k_weight, "k_weight", dtype, device), float(eps))
+    return device, (T, Hq, Hkv, D, bs, NB, dt), rows, turn
 
 
 def pa_rope_and_cache(query, key, value, query_out, k_pool, v_pool, slot_mapping, positions, cos_sin, pair_axes=None,
@@ -487,15 +506,12 @@ def pa_rope_and_cache(query, key, value, query_out, k_pool, v_pool, slot_mapping
     heads; query_out gets the queries, the pools the keys and values at
     slot_mapping.  query, key and value may be slices of one projection's
     output ([tokens, heads, head_dim], tokens apart)."""
-    T, Hq, Hkv, D, NB, bs, dt, rows, pos, weights = _rope_args(query, key, value, query_out, k_pool, v_pool, positions,
-                                                               cos_sin, pair_axes, q_weight, k_weight)
-    if slot_mapping.numel() != T or positions is None:
+    device, sizes, rows, turn = _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes,
+                                           interleaved, q_weight, k_weight, eps)
+    if slot_mapping.numel() != sizes[0] or positions is None:
         raise ValueError("slot_mapping and positions need one entry a token")
-    slots = _dev(slot_mapping, "slot_mapping", torch.int64)
-    with _device_guard(stream, query, key, value, query_out, k_pool, v_pool, slot_mapping, positions, cos_sin,
-                       pair_axes, q_weight, k_weight):
-        _check("pa_rope_and_cache", _lib.pa_rope_and_cache(
-            *rows, slots, *pos, int(interleaved), *weights, float(eps), T, Hq, Hkv, D, bs, NB, dt, _stream(stream)))
+    _call("pa_rope_and_cache", device, stream, *rows, _on(slot_mapping, "slot_mapping", torch.int64, device), *turn,
+          *sizes)
 
 
 def pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, cos_sin,
@@ -504,20 +520,16 @@ def pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block
     """pa_rope_and_cache of one decode step: token b is position
     context_lens[b] - 1 of sequence b, its slot comes from the block table, and
     it turns by that position unless `positions` gives others."""
-    B, Hq, Hkv, D, NB, bs, dt, rows, pos, weights = _rope_args(query, key, value, query_out, k_pool, v_pool, positions,
-                                                               cos_sin, pair_axes, q_weight, k_weight)
-    if block_tables.shape[0] != B or context_lens.numel() != B:
+    device, sizes, rows, turn = _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes,
+                                           interleaved, q_weight, k_weight, eps)
+    B, MBS = block_tables.shape
+    if B != sizes[0] or context_lens.numel() != B:
         raise ValueError("block_tables / context_lens do not match the batch of query")
     if slot_mapping is not None and slot_mapping.numel() != B:
         raise ValueError("slot_mapping needs one entry a sequence")
-    tables = _dev(block_tables, "block_tables", torch.int32)
-    lens = _dev(context_lens, "context_lens", torch.int32)
-    slots = _opt(slot_mapping, "slot_mapping", torch.int64)
-    with _device_guard(stream, query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, positions,
-                       cos_sin, pair_axes, q_weight, k_weight, slot_mapping):
-        _check("pa_rope_and_cache_decode", _lib.pa_rope_and_cache_decode(
-            *rows, tables, block_tables.shape[1], lens, *pos, int(interleaved), *weights, float(eps), B, Hq, Hkv, D,
-            bs, NB, dt, slots, _stream(stream)))
+    _call("pa_rope_and_cache_decode", device, stream, *rows, _on(block_tables, "block_tables", torch.int32, device), MBS,
+          _on(context_lens, "context_lens", torch.int32, device), *turn, *sizes,
+          _opt(slot_mapping, "slot_mapping", torch.int64, device))
 
 
 def pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, query_start=None, max_query_len: int = 1,
@@ -527,22 +539,22 @@ def pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, query_s
     query_start[b + 1] - query_start[b] of sequence b, or its last one."""
     NB, Hkv, bs, D = k_pool.shape
     B, MBS = block_tables.shape
-    if tuple(key_bounds.shape) != (NB, Hkv, 2, D):
+    if key_bounds.shape != (NB, Hkv, 2, D):
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
     if context_lens.numel() != B or (query_start is not None and query_start.numel() != B + 1):
         raise ValueError("context_lens needs batch entries, query_start batch + 1")
-    args = (_dev(k_pool, "k_pool"), _dev(key_bounds, "key_bounds", k_pool.dtype),
-            _dev(block_tables, "block_tables", torch.int32), MBS, _dev(context_lens, "context_lens", torch.int32),
-            _opt(query_start, "query_start", torch.int32), int(max_query_len), B, Hkv, D, bs, NB, _kv_dtype(k_pool))
-    with _device_guard(stream, k_pool, key_bounds, block_tables, context_lens, query_start):
-        _check("pa_update_key_bounds", _lib.pa_update_key_bounds(*args, _stream(stream)))
+    dt, device = _kv_dtype(k_pool), _device_of(k_pool, "k_pool")
+    _call("pa_update_key_bounds", device, stream, _on(k_pool, "k_pool", k_pool.dtype, device),
+          _on(key_bounds, "key_bounds", k_pool.dtype, device), _on(block_tables, "block_tables", torch.int32, device),
+          MBS, _on(context_lens, "context_lens", torch.int32, device),
+          _opt(query_start, "query_start", torch.int32, device), int(max_query_len), B, Hkv, D, bs, NB, dt)
 
 
-def _row_args(rows: int, block_tables, seq_ids, context_lens):
+def _row_args(rows: int, block_tables, seq_ids, context_lens, device: int):
     if context_lens.numel() != rows or (seq_ids is not None and seq_ids.numel() != rows):
         raise ValueError("context_lens and seq_ids need one entry a query row")
-    return (_dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-            _opt(seq_ids, "seq_ids", torch.int32), _dev(context_lens, "context_lens", torch.int32))
+    return (_on(block_tables, "block_tables", torch.int32, device), block_tables.shape[1],
+            _opt(seq_ids, "seq_ids", torch.int32, device), _on(context_lens, "context_lens", torch.int32, device))
 
 
 def pa_block_scores(q, key_bounds, block_tables, context_lens, max_context_len: int, block_size: int, scores,
@@ -552,13 +564,13 @@ def pa_block_scores(q, key_bounds, block_tables, context_lens, max_context_len: 
     [rows, Hkv, >= ceil(max_context_len / block_size)])."""
     R, Hq, D = q.shape
     NB, Hkv, two, D2 = key_bounds.shape
-    if D2 != D or two != 2 or scores.dim() != 3 or tuple(scores.shape[:2]) != (R, Hkv):
+    if D2 != D or two != 2 or scores.dim() != 3 or scores.shape[:2] != (R, Hkv):
         raise ValueError("q / key_bounds / scores shapes disagree")
-    args = (_dev(q, "q"), _dev(key_bounds, "key_bounds", q.dtype), *_row_args(R, block_tables, seq_ids, context_lens),
-            int(max_context_len), int(block_size), _dev(scores, "scores", torch.float32), scores.shape[2], R,
-            block_tables.shape[0], Hq, Hkv, D, NB, _kv_dtype(q))
-    with _device_guard(stream, q, key_bounds, block_tables, context_lens, scores, seq_ids):
-        _check("pa_block_scores", _lib.pa_block_scores(*args, _stream(stream)))
+    dt, device = _kv_dtype(q), _device_of(q, "q")
+    _call("pa_block_scores", device, stream, _on(q, "q", q.dtype, device),
+          _on(key_bounds, "key_bounds", q.dtype, device), *_row_args(R, block_tables, seq_ids, context_lens, device),
+          int(max_context_len), int(block_size), _on(scores, "scores", torch.float32, device), scores.shape[2], R,
+          block_tables.shape[0], Hq, Hkv, D, NB, dt)
 
 
 def pa_select_blocks(scores, context_lens, max_context_len: int, block_size: int, selected, num_first: int = 1,
@@ -567,13 +579,12 @@ def pa_select_blocks(scores, context_lens, max_context_len: int, block_size: int
     num_first and last num_last blocks and those of the largest score, in
     ascending order, -1 behind them."""
     R, Hkv, S = scores.shape
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (R, Hkv) or context_lens.numel() != R:
+    if selected.dim() != 3 or selected.shape[:2] != (R, Hkv) or context_lens.numel() != R:
         raise ValueError("scores / selected / context_lens shapes disagree")
-    args = (_dev(scores, "scores", torch.float32), S, _dev(context_lens, "context_lens", torch.int32),
-            int(max_context_len), int(block_size), _dev(selected, "selected", torch.int32), selected.shape[2],
-            int(num_first), int(num_last), R, Hkv)
-    with _device_guard(stream, scores, context_lens, selected):
-        _check("pa_select_blocks", _lib.pa_select_blocks(*args, _stream(stream)))
+    device = _device_of(scores, "scores")
+    _call("pa_select_blocks", device, stream, _on(scores, "scores", torch.float32, device), S,
+          _on(context_lens, "context_lens", torch.int32, device), int(max_context_len), int(block_size),
+          _on(selected, "selected", torch.int32, device), selected.shape[2], int(num_first), int(num_last), R, Hkv)
 
 
 def pa_paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens, selected, scale: float, out,
@@ -582,13 +593,14 @@ def pa_paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_le
     selected[r, g] lists (negative entries name no block)."""
     R, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_pool.shape
-    if D2 != D or v_pool.shape != k_pool.shape or tuple(out.shape) != (R, Hq, D):
+    if D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape:
         raise ValueError("q / pool / out shapes disagree")
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (R, Hkv):
+    if selected.dim() != 3 or selected.shape[:2] != (R, Hkv):
         raise ValueError("selected must be [rows, num_kv_heads, max_selected]")
-    args = (_dev(q, "q"), _dev(k_pool, "k_pool", q.dtype), _dev(v_pool, "v_pool", q.dtype),
-            *_row_args(R, block_tables, seq_ids, context_lens), _dev(selected, "selected", torch.int32),
-            selected.shape[2], float(scale), bs, _dev(out, "out"), _kv_dtype(out), R, block_tables.shape[0], Hq, Hkv,
-            D, NB, _kv_dtype(q))
-    with _device_guard(stream, q, k_pool, v_pool, block_tables, context_lens, selected, out, seq_ids):
-        _check("pa_paged_attention_decode_sparse", _lib.pa_paged_attention_decode_sparse(*args, _stream(stream)))
+    dtype, dt, out_dt = q.dtype, _kv_dtype(q), _kv_dtype(out)
+    device = _device_of(q, "q")
+    _call("pa_paged_attention_decode_sparse", device, stream, _on(q, "q", dtype, device),
+          _on(k_pool, "k_pool", dtype, device), _on(v_pool, "v_pool", dtype, device),
+          *_row_args(R, block_tables, seq_ids, context_lens, device), _on(selected, "selected", torch.int32, device),
+          selected.shape[2], float(scale), bs, _on(out, "out", out.dtype, device), out_dt, R, block_tables.shape[0], Hq, Hkv, D,
+          NB, dt)
