@@ -30,7 +30,6 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeWarps = 4;
 
 enum Pairing {
     kNeighbours,  // (2p, 2p + 1)
@@ -65,19 +64,19 @@ struct RopeParams {
     int* err;
 };
 
+// One warp is one CTA, so that all that depends on its token and step alone is
+// the same for the whole CTA and stays off the lanes.
 template <typename T, int D, Pairing PAIRING, bool DECODE>
-__global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const RopeParams p) {
-    constexpr int kLanes = D / kChunk;           // lanes of one head row
-    constexpr int kHeads = 32 / kLanes;          // head rows of a step
+__global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) {
+    constexpr int kLanes = D / kChunk;              // lanes of one head row
+    constexpr int kHeads = 32 / kLanes;             // head rows of a step
     constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // steps loaded together, 16 registers
-    __shared__ __align__(16) float angles[kRopeWarps][2][D / 2];
+    __shared__ __align__(16) float cs[2][D / 2];    // the token's cosines and sines
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-    const int64_t token = unit / p.slices;
-    if (token >= p.num_tokens) return;  // whole warps
-    const int slice = (int)(unit - token * p.slices);
-    const int lane = threadIdx.x & 31;
+    const int64_t token = blockIdx.x / p.slices;
+    const int slice = (int)(blockIdx.x - token * p.slices);
+    const int lane = threadIdx.x;
     const int sub = lane / kLanes, x = lane % kLanes;
     // the lane's elements: 8 from `own`, or 4 there and 4 in the other half
     const int own = PAIRING == kWholeHalves ? x * 4 : x * 8;
@@ -85,25 +84,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const Ro
 
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
     const int q_steps = (Hq + kHeads - 1) / kHeads, kv_steps = (Hkv + kHeads - 1) / kHeads;
-    const int first = slice * p.steps, end = min(first + p.steps, q_steps + 2 * kv_steps);
-    const T* q_src = static_cast<const T*>(p.query) + token * p.q_stride + own;
-    const T* k_src = static_cast<const T*>(p.key) + token * p.k_stride + own;
-    const T* v_src = static_cast<const T*>(p.value) + token * p.v_stride + own;
+    const int v_first = q_steps + kv_steps;
+    const int first = slice * p.steps, end = min(first + p.steps, v_first + kv_steps);
+    const T* q_src = static_cast<const T*>(p.query) + token * p.q_stride;
+    const T* k_src = static_cast<const T*>(p.key) + token * p.k_stride;
+    const T* v_src = static_cast<const T*>(p.value) + token * p.v_stride;
+    const int src_lane = sub * D + own;
     Chunk<T> rows[kAhead];
     auto load = [&](Chunk<T>(&to)[kAhead], int from) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int s = from + u;  // the same for every lane
-            const T* src = s < q_steps ? q_src : s < q_steps + kv_steps ? k_src : v_src;
-            const int head = (s < q_steps ? s : s < q_steps + kv_steps ? s - q_steps : s - q_steps - kv_steps) * kHeads + sub;
+            const int st = from + u;
+            const int head = (st < q_steps ? st : st < v_first ? st - q_steps : st - v_first) * kHeads;
+            const T* src = (st < q_steps ? q_src : st < v_first ? k_src : v_src) + (int64_t)head * D;
             to[u] = Chunk<T>{};
-            if (s < end && head < (s < q_steps ? Hq : Hkv)) to[u].load(src + (int64_t)head * D, src + (int64_t)head * D + kOther);
+            if (st < end && head + sub < (st < q_steps ? Hq : Hkv)) to[u].load(src + src_lane, src + src_lane + kOther);
         }
     };
     load(rows, first);  // beside the look-up of where they go
-    Chunk<T> wq{}, wk{};
-    if (p.q_weight) wq.load(static_cast<const T*>(p.q_weight) + own, static_cast<const T*>(p.q_weight) + own + kOther);
-    if (p.k_weight) wk.load(static_cast<const T*>(p.k_weight) + own, static_cast<const T*>(p.k_weight) + own + kOther);
 
     // where the token goes
     int64_t slot = -1, text_pos = -1;
@@ -124,7 +122,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const Ro
     }
     // its angles, a pair or two a lane; a bad position or axis reads nothing
     const int half = p.rotary_dim / 2;
-    float(*cs)[D / 2] = angles[threadIdx.x >> 5];
     if (DECODE ? text_pos >= 0 : slot >= 0) {
 #pragma unroll
         for (int i = 0; i < D / 2; i += 32) {
@@ -141,39 +138,65 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const Ro
             }
         }
     }
-    bad = __any_sync(0xffffffffu, bad);  // and the angles are in for every lane
+    bad = __any_sync(0xffffffffu, bad);
     const bool write = slot >= 0 && !bad;
     if (slice == 0 && lane == 0) {
         if (bad) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
         if (p.slots_out) p.slots_out[token] = write ? slot : -1;
     }
     if (!write) return;  // the same for every lane
-    __syncwarp();
+    __syncwarp();        // the angles are in
 
-    // cosine and sine of the lane's pairs
-    constexpr int kPairs = PAIRING == kHalves ? 8 : 4;
+    // Coefficients of the lane's elements, weights multiplied in.  Both elements
+    // of a pair in the lane: (y1, y2) -> (y1 f[0] - y2 f[1], y2 f[2] + y1 f[3]),
+    // four pairs.  Across lanes (kHalves): y f[0..1] is the weighted row, f[2..3]
+    // cosines and f[4..5] signed sines, 8 elements each.
+    constexpr bool kInLane = PAIRING != kHalves;
     const bool turned = PAIRING == kWholeHalves || x * kChunk < p.rotary_dim;
     const int shift = p.rotary_dim / (2 * kChunk);  // kHalves: lanes between the elements of a pair
     const bool second = PAIRING == kHalves && x >= shift;
     const int partner = !turned ? lane : second ? lane - shift : lane + shift;
-    float c[kPairs], s[kPairs];
-    {
-        const int at = PAIRING == kHalves ? (second ? x - shift : x) * 8 : x * 4;
+    float f[kInLane ? 4 : 6][4];
+    auto coefficients = [&](const void* weight) {
+        float w[kChunk];
+        if (weight) {
+            Chunk<T> c;
+            c.load(static_cast<const T*>(weight) + own, static_cast<const T*>(weight) + own + kOther);
+            c.to_f32(w);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPairs; i += 4) {
-            const float4 a = turned ? *reinterpret_cast<const float4*>(&cs[0][at + i]) : float4{};
-            const float4 b = turned ? *reinterpret_cast<const float4*>(&cs[1][at + i]) : float4{};
-            c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
-            s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
+            for (int i = 0; i < kChunk; ++i) w[i] = 1.f;
         }
-    }
+        if (kInLane) {
+            const float4 a = turned ? *reinterpret_cast<const float4*>(&cs[0][x * 4]) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 b = turned ? *reinterpret_cast<const float4*>(&cs[1][x * 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float c[4] = {a.x, a.y, a.z, a.w}, s[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w1 = w[PAIRING == kWholeHalves ? i : 2 * i], w2 = w[PAIRING == kWholeHalves ? i + 4 : 2 * i + 1];
+                f[0][i] = w1 * c[i];
+                f[1][i] = w2 * s[i];
+                f[2][i] = w2 * c[i];
+                f[3][i] = w1 * s[i];
+            }
+        } else {
+            const int at = turned ? (second ? x - shift : x) * 8 : 0;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                f[i / 4][i % 4] = w[i];
+                f[kInLane ? 0 : 2 + i / 4][i % 4] = cs[0][at + i];
+                f[kInLane ? 0 : 4 + i / 4][i % 4] = second ? cs[1][at + i] : -cs[1][at + i];
+            }
+        }
+    };
     const int64_t blk = slot / p.block_size;
     const int off = (int)(slot - blk * p.block_size);
-    T* q_dst = static_cast<T*>(p.query_out) + token * Hq * D + own;
-    const int64_t pool_row = ((blk * Hkv) * p.block_size + off) * D + own;  // kv head 0
+    T* q_dst = static_cast<T*>(p.query_out) + token * Hq * D;
+    const int64_t pool_row = ((blk * Hkv) * p.block_size + off) * D;  // kv head 0
     T* k_dst = static_cast<T*>(p.k_pool) + pool_row;
     T* v_dst = static_cast<T*>(p.v_pool) + pool_row;
     const int64_t head_stride = (int64_t)p.block_size * D;  // between kv heads in the pool
+    const int64_t pool_lane = sub * head_stride + own;
 
     for (int from = first; from < end; from += kAhead) {
         Chunk<T> next[kAhead];
@@ -182,8 +205,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const Ro
         for (int u = 0; u < kAhead; ++u) {
             const int st = from + u;
             if (st >= end) break;
-            const bool is_q = st < q_steps, is_v = st >= q_steps + kv_steps;
+            const bool is_q = st < q_steps, is_v = st >= v_first;
+            const int head = (is_q ? st : is_v ? st - v_first : st - q_steps) * kHeads;
             if (!is_v) {
+                if (st == first || st == q_steps) coefficients(is_q ? p.q_weight : p.k_weight);
                 float y[kChunk];
                 rows[u].to_f32(y);
                 if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
@@ -193,31 +218,35 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_cache_kernel(const Ro
 #pragma unroll
                     for (int m = kLanes / 2; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                     const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
-                    float w[kChunk];
-                    (is_q ? wq : wk).to_f32(w);
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) y[i] = y[i] * inv * w[i];
+                    for (int i = 0; i < kChunk; ++i) y[i] *= inv;
                 }
-                if (PAIRING == kHalves) {
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        const float z = __shfl_sync(0xffffffffu, y[i], partner);
-                        if (turned) y[i] = fmaf(y[i], c[i % kPairs], second ? z * s[i % kPairs] : -(z * s[i % kPairs]));
-                    }
-                } else if (turned) {
+                if (kInLane) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int a = PAIRING == kWholeHalves ? i : 2 * i, b = PAIRING == kWholeHalves ? i + 4 : 2 * i + 1;
                         const float y1 = y[a], y2 = y[b];
-                        y[a] = fmaf(y1, c[i], -(y2 * s[i]));
-                        y[b] = fmaf(y2, c[i], y1 * s[i]);
+                        if (turned) {
+                            y[a] = fmaf(y1, f[0][i], -(y2 * f[1][i]));
+                            y[b] = fmaf(y2, f[2][i], y1 * f[3][i]);
+                        } else {
+                            y[a] = y1 * f[0][i];
+                            y[b] = y2 * f[2][i];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) {
+                        y[i] *= f[i / 4][i % 4];
+                        const float z = __shfl_sync(0xffffffffu, y[i], partner);
+                        if (turned) y[i] = fmaf(y[i], f[kInLane ? 0 : 2 + i / 4][i % 4], z * f[kInLane ? 0 : 4 + i / 4][i % 4]);
                     }
                 }
                 rows[u].from_f32(y);
             }
-            const int head = (is_q ? st : is_v ? st - q_steps - kv_steps : st - q_steps) * kHeads + sub;
-            T* dst = is_q ? q_dst + (int64_t)head * D : (is_v ? v_dst : k_dst) + head * head_stride;
-            if (head < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + kOther);
+            T* dst = is_q ? q_dst + (int64_t)head * D + src_lane
+                          : (is_v ? v_dst : k_dst) + head * head_stride + pool_lane;
+            if (head + sub < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + kOther);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) rows[u] = next[u];
@@ -240,12 +269,12 @@ int launch_rope(RopeParams p, bool interleaved, cudaStream_t stream) {
     per_warp = std::max((int64_t)1, std::min(per_warp, steps));
     p.slices = (int)((steps + per_warp - 1) / per_warp);
     p.steps = (int)((steps + p.slices - 1) / p.slices);  // evened out
-    const int64_t blocks = (p.num_tokens * p.slices + kRopeWarps - 1) / kRopeWarps;
+    const int64_t blocks = p.num_tokens * p.slices;
     if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     auto kernel = interleaved            ? rope_cache_kernel<T, D, kNeighbours, DECODE>
                   : p.rotary_dim == D    ? rope_cache_kernel<T, D, kWholeHalves, DECODE>
                                          : rope_cache_kernel<T, D, kHalves, DECODE>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRopeWarps * 32), 0, stream, p);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32), 0, stream, p);
 }
 
 // Checks that both entry points share, then the launch.
