@@ -420,16 +420,17 @@ def _device_of(t, name: str) -> int:
     return t.get_device()
 
 
+_Tensor = torch.Tensor
+
+
 def _on(t, name: str, dtype, device: int) -> int:
     """Pointer of a contiguous tensor of this type on this device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or not t.is_contiguous():
-        _refuse(t, name, dtype, device)
-    return t.data_ptr()
-
-
-def _refuse(t, name: str, dtype, device: int) -> None:
-    _dev(t, name, dtype)
-    raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
+    if t.__class__ is _Tensor and t.get_device() == device and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    pointer = _dev(t, name, dtype)  # names what is wrong, or takes a subclass
+    if t.get_device() != device:
+        raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
+    return pointer
 
 
 def _opt(t, name: str, dtype, device: int):
@@ -437,9 +438,12 @@ def _opt(t, name: str, dtype, device: int):
 
 
 def _call(name: str, device: int, stream, *args) -> None:
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
+        raw = _stream(stream)
     if device == torch.cuda.current_device():
         status = getattr(_lib, name)(*args, raw)
     else:
@@ -452,11 +456,11 @@ def _call(name: str, device: int, stream, *args) -> None:
 def _token_rows(t, name: str, T: int, H: int, D: int, dtype, device: int) -> tuple[int, int]:
     """Pointer and token stride of [tokens, heads, head_dim] rows whose tokens
     may lie apart (a slice of one projection's output)."""
-    if _device_of(t, name) != device:
-        raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (T, H, D):
+    if t.get_device() != device or t.dtype is not dtype or t.shape != (T, H, D):
+        if _device_of(t, name) != device:
+            raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
     st = t.stride()
     if st[2] != 1 or (H > 1 and st[1] != D):

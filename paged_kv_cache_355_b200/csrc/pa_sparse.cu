@@ -42,161 +42,7 @@ __device__ __forceinline__ void store_out(const SparseParams& p, int64_t at, flo
         static_cast<float*>(p.out)[at] = x;
 }
 
-constexpr int kSimtWarps = 8;
-
-// CUDA-core form.  One CTA per (row, kv head, G query heads); its warps take
-// the listed blocks in turn.  D / 8 lanes hold one token's row; each such lane
-// group keeps its own running maximum, sum and output, joined at the end.
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kSimtWarps * 32) sparse_simt_kernel(const SparseParams p, int head_slices) {
-    constexpr int kLanes = D / kChunk;
-    constexpr int kRows = 32 / kLanes;
-    constexpr int kStates = kSimtWarps * kRows;
-    __shared__ float s_m[kStates][G], s_l[kStates][G];
-    __shared__ float s_o[kSimtWarps][G][D];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t unit = blockIdx.x;
-    const int64_t rg = unit / head_slices;  // (row, kv head)
-    const int slice = (int)(unit - rg * head_slices);
-    const int64_t row = rg / p.num_kv_heads;
-    const int h = (int)(rg - row * p.num_kv_heads);
-    const int head0 = h * (p.num_q_heads / p.num_kv_heads) + slice * G;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane / kLanes, chunk = lane % kLanes;
-
-    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
-    const int L = p.context_lens[row];
-    bool row_ok = seq >= 0 && seq < p.batch && L >= 0 && L <= (int64_t)p.max_blocks_per_seq * p.block_size;
-    if (!row_ok && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-    const int32_t* table = p.block_tables + (row_ok ? seq : 0) * p.max_blocks_per_seq;
-    const int32_t* list = p.selected + rg * p.max_selected;
-
-    float q[G][kChunk], o[G][kChunk], m[G], l[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        Chunk<T> raw;
-        raw.load(static_cast<const T*>(p.q) + (row * p.num_q_heads + head0 + g) * D + chunk * kChunk);
-        raw.to_f32(q[g]);
-        m[g] = __int_as_float(0xff800000);
-        l[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            q[g][e] *= p.scale_log2;
-            o[g][e] = 0.f;
-        }
-    }
-    for (int i = warp; row_ok && i < p.max_selected; i += kSimtWarps) {
-        const int j = list[i];
-        if (j < 0) continue;
-        int64_t blk = -1;
-        if ((int64_t)j * p.block_size < L) blk = table[j];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-            continue;
-        }
-        const int held = min(p.block_size, L - j * p.block_size);
-        const int64_t base = ((blk * p.num_kv_heads + h) * p.block_size) * D + chunk * kChunk;
-        for (int t0 = 0; t0 < held; t0 += kRows) {
-            const int t = t0 + sub;
-            const bool in = t < held;
-            float k[kChunk] = {}, v[kChunk] = {};
-            if (in) {
-                Chunk<T> raw;
-                raw.load(static_cast<const T*>(p.k_pool) + base + t * D);
-                raw.to_f32(k);
-                raw.load(static_cast<const T*>(p.v_pool) + base + t * D);
-                raw.to_f32(v);
-            }
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < kChunk; ++e) s = fmaf(q[g][e], k[e], s);
-#pragma unroll
-                for (int x = kLanes / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                if (!in) continue;
-                const float top = fmaxf(m[g], s);
-                const float base_m = top == __int_as_float(0xff800000) ? 0.f : top;
-                const float keep = exp2f(m[g] - base_m), w = exp2f(s - base_m);
-                m[g] = top;
-                l[g] = l[g] * keep + w;
-#pragma unroll
-                for (int e = 0; e < kChunk; ++e) o[g][e] = fmaf(w, v[e], o[g][e] * keep);
-            }
-        }
-    }
-    // join the lane groups and warps
-    const int state = warp * kRows + sub;
-    if (chunk == 0) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            s_m[state][g] = m[g];
-            s_l[state][g] = l[g];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        float top = __int_as_float(0xff800000);
-        for (int x = 0; x < kStates; ++x) top = fmaxf(top, s_m[x][g]);
-        const float base_m = top == __int_as_float(0xff800000) ? 0.f : top;
-        const float w = exp2f(m[g] - base_m);
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            float x = o[g][e] * w;
-#pragma unroll
-            for (int y = kLanes; y < 32; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-            if (sub == 0) s_o[warp][g][chunk * kChunk + e] = x;
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += kSimtWarps * 32) {
-        const int g = i / D, d = i - g * D;
-        float top = __int_as_float(0xff800000);
-        for (int x = 0; x < kStates; ++x) top = fmaxf(top, s_m[x][g]);
-        const float base_m = top == __int_as_float(0xff800000) ? 0.f : top;
-        float sum = 0.f, acc = 0.f;
-        for (int x = 0; x < kStates; ++x) sum += s_l[x][g] * exp2f(s_m[x][g] - base_m);
-#pragma unroll
-        for (int x = 0; x < kSimtWarps; ++x) acc += s_o[x][g][d];
-        // nothing attended: a zero row (a NaN sum stays NaN)
-        store_out(p, (row * p.num_q_heads + head0 + g) * D + d, sum == 0.f ? 0.f : acc / sum);
-    }
-}
-
-template <typename T, int D>
-int launch_simt(const SparseParams& p, cudaStream_t st) {
-    const int group = p.num_q_heads / p.num_kv_heads;
-    const int slices = group > 8 ? group / 8 : 1;
-    const int64_t grid = p.num_rows * p.num_kv_heads * slices;
-    if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    const dim3 g((unsigned)grid), b(kSimtWarps * 32);
-    switch (group / slices) {
-        case 1: return launch_pdl(sparse_simt_kernel<T, D, 1>, g, b, 0, st, p, slices);
-        case 2: return launch_pdl(sparse_simt_kernel<T, D, 2>, g, b, 0, st, p, slices);
-        case 4: return launch_pdl(sparse_simt_kernel<T, D, 4>, g, b, 0, st, p, slices);
-        case 8: return launch_pdl(sparse_simt_kernel<T, D, 8>, g, b, 0, st, p, slices);
-    }
-    return PA_ERR_UNSUPPORTED;
-}
-
-// ---------------------------------------------------------------------------
-// bf16: matrix instructions
-// ---------------------------------------------------------------------------
-// A warp takes 16 tokens at a time (two half-tiles of 8, so that blocks of 8,
-// 16 and 32 tokens are all whole half-tiles) through a ring of shared memory of
-// its own, filled by asynchronous copies: warps never wait for one another
-// until the end.  Both products are m16n8k16 with the few query heads on the
-// 8-wide side: S^T = K Q^T over 16 tokens, O^T = V^T P^T over 16 channels at a
-// time, so no row of an instruction is padding.  P^T's fragment is S^T's
-// accumulator, rounded and transposed in 8x8 matrices between the lanes.
-// 16-byte chunk c of a row lies at c ^ (row & 7), so that the eight rows of a
-// matrix load touch all banks.
-// P is split into a bf16 value and a bf16 remainder (two products), so that
-// its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
-// once (2^-9) would be half of a bf16 output's own error.
-constexpr int kMmaWarps = 4;
+constexpr int kSparseWarps = 4;
 constexpr int kMaxSplits = 8;  // the portable cluster size
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -225,13 +71,129 @@ __device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
     return x;
 }
 
+// What both kernels know of their (row, kv head), and of the half-tiles of 8
+// tokens that its list names.
+struct Row {
+    int64_t unit, row;
+    int h, group, L;
+    bool ok;
+    const int32_t *table, *list;
+    uint32_t rank;  // of the CTA in the list's cluster
+
+    // Reads the list's entry of half-tile `half` beside the row's length.
+    __device__ __forceinline__ int open(const SparseParams& p, int splits, int64_t half, int64_t halves, int shift) {
+        unit = blockIdx.x / splits;
+        row = unit / p.num_kv_heads;
+        h = (int)(unit - row * p.num_kv_heads);
+        group = p.num_q_heads / p.num_kv_heads;
+        list = p.selected + unit * p.max_selected;
+        const int entry = half < halves ? list[half >> shift] : -1;
+        const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
+        L = p.context_lens[row];
+        ok = seq >= 0 && seq < p.batch && L >= 0 && L <= (int64_t)p.max_blocks_per_seq * p.block_size;
+        if (!ok && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+        table = p.block_tables + (ok ? seq : 0) * p.max_blocks_per_seq;
+        return entry;
+    }
+    // The place in the pools, in rows of 8 tokens, of the sub-th half-tile of
+    // listed block j, and its tokens below L (0: nothing to read).
+    __device__ __forceinline__ int place(const SparseParams& p, int j, int sub, int per_block, uint32_t& at) const {
+        at = 0;
+        if (j < 0) return 0;
+        int64_t blk = -1;
+        if ((int64_t)j * p.block_size < L) blk = table[j];
+        if (blk < 0 || blk >= p.num_blocks) {
+            record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+            return 0;
+        }
+        at = (uint32_t)((blk * p.num_kv_heads + h) * per_block + sub);
+        return min(8, max(0, L - j * p.block_size - 8 * sub));
+    }
+};
+
+// Joins the states (running maximum, sum and output of each head) that the
+// CTA's threads left in shared memory, then those of the cluster's CTAs, each
+// CTA finishing its share of the outputs.
+template <int STATES, int HEADS, int D>
+__device__ __forceinline__ void join_states(const SparseParams& p, const Row& r, int splits, float (*s_o)[HEADS][D],
+                                            float (*s_m)[HEADS], float (*s_l)[HEADS], float* c_m, float* c_l) {
+    const float kNegInf = __int_as_float(0xff800000);
+    constexpr int kThreads = kSparseWarps * 32;
+    const int64_t out0 = (r.row * p.num_q_heads + r.h * r.group) * D;
+    __syncthreads();
+    for (int i = threadIdx.x; i < r.group * D; i += kThreads) {
+        const int head = i / D, d = i % D;
+        float top = kNegInf;
+#pragma unroll
+        for (int w = 0; w < STATES; ++w) top = fmaxf(top, s_m[w][head]);
+        const float base = top == kNegInf ? 0.f : top;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < STATES; ++w) {
+            const float weight = exp2f(s_m[w][head] - base);
+            sum = fmaf(s_l[w][head], weight, sum);
+            acc = fmaf(s_o[w][head][d], weight, acc);
+        }
+        if (splits == 1) {
+            // nothing attended: a zero row (a NaN sum stays NaN)
+            store_out(p, out0 + i, sum == 0.f ? 0.f : acc / sum);
+        } else {
+            s_o[0][head][d] = acc;  // read by this thread alone until here
+            if (d == 0) {
+                c_m[head] = top;
+                c_l[head] = sum;
+            }
+        }
+    }
+    if (splits == 1) return;
+    cluster_sync();
+    for (int i = r.rank * kThreads + threadIdx.x; i < r.group * D; i += splits * kThreads) {
+        const int head = i / D, d = i % D;
+        float ms[kMaxSplits], ls[kMaxSplits], os[kMaxSplits];
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) {
+            ms[c] = c < splits ? load_cluster(&c_m[head], c) : kNegInf;
+            ls[c] = c < splits ? load_cluster(&c_l[head], c) : 0.f;
+            os[c] = c < splits ? load_cluster(&s_o[0][head][d], c) : 0.f;
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) top = fmaxf(top, ms[c]);
+        const float base = top == kNegInf ? 0.f : top;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) {
+            const float weight = exp2f(ms[c] - base);
+            sum = fmaf(ls[c], weight, sum);
+            acc = fmaf(os[c], weight, acc);
+        }
+        store_out(p, out0 + i, sum == 0.f ? 0.f : acc / sum);
+    }
+    cluster_sync();  // the shared memory lives until the cluster has read it
+}
+
+// ---------------------------------------------------------------------------
+// bf16: matrix instructions
+// ---------------------------------------------------------------------------
+// A warp takes 16 tokens at a time (two half-tiles of 8, so that blocks of 8,
+// 16 and 32 tokens are all whole half-tiles) through a ring of shared memory of
+// its own, filled by asynchronous copies: warps never wait for one another
+// until the end.  Both products are m16n8k16 with the few query heads on the
+// 8-wide side: S^T = K Q^T over 16 tokens, O^T = V^T P^T over 16 channels at a
+// time, so no row of an instruction is padding.  P^T's fragment is S^T's
+// accumulator, rounded and transposed in 8x8 matrices between the lanes.
+// 16-byte chunk c of a row lies at c ^ (row & 7), so that the eight rows of a
+// matrix load touch all banks.
+// P is split into a bf16 value and a bf16 remainder (two products), so that
+// its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
+// once (2^-9) would be half of a bf16 output's own error.
 // One cluster of `splits` CTAs per (row, kv head): its splits * 4 warps take
 // the tiles of the list in turn, each with its own running maximum and sum, and
 // the states are joined through the cluster's shared memory, so that a long
 // list of few rows fills the GPU without a workspace or a second launch.
 // NT: 8-wide tiles of query heads (2 for a group of 16).
 template <int D, int NT, int kStages>
-__global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const SparseParams p, int splits) {
+__global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const SparseParams p, int splits) {
     constexpr int kHeads = 8 * NT;             // query heads, the group padded with zero rows
     constexpr int kRowBytes = 2 * D;
     constexpr int kTile = 16 * kRowBytes;      // K or V of one tile of 16 tokens
@@ -240,15 +202,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const Spa
     constexpr int kRowLanes = D / 8;           // lanes that copy one row
     constexpr int kCopyRows = 32 / kRowLanes;  // rows of one copy instruction
     extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][K, V][16 tokens][D], later the states
-    __shared__ float s_m[kMmaWarps][kHeads], s_l[kMmaWarps][kHeads], c_m[kHeads], c_l[kHeads];
+    __shared__ float s_m[kSparseWarps][kHeads], s_l[kSparseWarps][kHeads], c_m[kHeads], c_l[kHeads];
     const float kNegInf = __int_as_float(0xff800000);
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t rank = splits > 1 ? cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / splits;
-    const int64_t row = unit / p.num_kv_heads;
-    const int h = (int)(unit - row * p.num_kv_heads);
-    const int group = p.num_q_heads / p.num_kv_heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
@@ -258,18 +215,13 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const Spa
     const int per_block = p.block_size / 8;  // half-tiles
     const int shift = per_block == 1 ? 0 : per_block == 2 ? 1 : 2;
     const int64_t halves = (int64_t)p.max_selected * per_block;
-    const int step = splits * kMmaWarps;     // warps of the cluster
+    const int step = splits * kSparseWarps;  // warps of the cluster
     const int64_t tiles = (halves + 1) / 2;
-    const int32_t* list = p.selected + unit * p.max_selected;
-    int64_t first = (int64_t)rank * kMmaWarps + warp;
+    Row r;
+    r.rank = splits > 1 ? cluster_rank() : 0;
+    int64_t first = (int64_t)r.rank * kSparseWarps + warp;
     int64_t half = (first + (int64_t)(lane >> 1) * step) * 2 + (lane & 1);
-    int entry = half < halves ? list[half >> shift] : -1;
-
-    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
-    const int L = p.context_lens[row];
-    const bool row_ok = seq >= 0 && seq < p.batch && L >= 0 && L <= (int64_t)p.max_blocks_per_seq * p.block_size;
-    if (!row_ok && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-    const int32_t* table = p.block_tables + (row_ok ? seq : 0) * p.max_blocks_per_seq;
+    int entry = r.open(p, splits, half, halves, shift);
 
     // the lane's part of the copies: one chunk of one row in every kCopyRows
     const int copy_row = lane / kRowLanes, copy_chunk = lane % kRowLanes;
@@ -287,34 +239,23 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const Spa
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int head = 8 * n + g;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (row * p.num_q_heads + h * group + head) * D + 2 * t;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (r.row * p.num_q_heads + r.h * r.group + head) * D + 2 * t;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                q[n][i][c] = head < group ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c) : 0u;
+                q[n][i][c] = head < r.group ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c) : 0u;
     }
     float o[NT][kSteps][4] = {};     // channels 16 i + g (+ 8), heads 8 n + 2 t (+ 1)
     float m[NT][2], l[NT][2] = {};   // of heads 8 n + 2 t (+ 1); l over this lane's tokens
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf;
 
-    for (; first < tiles && row_ok; first += (int64_t)step * 16) {
-        uint32_t at = 0;  // the half-tile's place in the pools, in rows of 8 tokens
-        int held = 0;     // its tokens below L
-        const int j = entry, sub = (int)(half & (per_block - 1));
+    for (; first < tiles && r.ok; first += (int64_t)step * 16) {
+        uint32_t at;
+        const int held = r.place(p, entry, (int)(half & (per_block - 1)), per_block, at);
         half += (int64_t)step * 32;
-        entry = half < halves ? list[half >> shift] : -1;
-        if (j >= 0) {
-            int64_t blk = -1;
-            if ((int64_t)j * p.block_size < L) blk = table[j];
-            if (blk < 0 || blk >= p.num_blocks) {
-                record_error(p.err, PA_ERR_BAD_BLOCK_ID);
-            } else {
-                held = min(8, max(0, L - j * p.block_size - 8 * sub));
-                at = (uint32_t)((blk * p.num_kv_heads + h) * per_block + sub);
-            }
-        }
+        entry = half < halves ? r.list[half >> shift] : -1;
         unsigned todo = __ballot_sync(0xffffffffu, held > 0);
         todo = (todo | (todo >> 1)) & 0x55555555u;
 
@@ -415,8 +356,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const Spa
         }
     }
 
-    // the warps' states, in the ring's place, joined to the CTA's; then the
-    // cluster's, each CTA finishing its share of the outputs
+    // the warps' states take the ring's place
     copy_async_wait<0>();
     __syncthreads();
     float(*s_o)[kHeads][D] = reinterpret_cast<float(*)[kHeads][D]>(ring);
@@ -437,71 +377,186 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 3) sparse_mma_kernel(const Spa
                 s_o[warp][head][16 * i + g + 8] = o[n][i][c + 2];
             }
         }
-    __syncthreads();
-    const bool alone = splits == 1;
-    for (int i = threadIdx.x; i < group * D; i += kMmaWarps * 32) {
-        const int head = i / D, d = i % D;
-        float top = kNegInf;
-#pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s_m[w][head]);
-        const float base = top == kNegInf ? 0.f : top;
-        float sum = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) {
-            const float weight = exp2f(s_m[w][head] - base);
-            sum = fmaf(s_l[w][head], weight, sum);
-            acc = fmaf(s_o[w][head][d], weight, acc);
-        }
-        if (alone) {
-            // nothing attended: a zero row (a NaN sum stays NaN)
-            store_out(p, (row * p.num_q_heads + h * group + head) * D + d, sum == 0.f ? 0.f : acc / sum);
-        } else {
-            s_o[0][head][d] = acc;  // read by this thread alone until here
-            if (d == 0) {
-                c_m[head] = top;
-                c_l[head] = sum;
-            }
-        }
-    }
-    if (alone) return;
-    cluster_sync();
-    for (int i = rank * (kMmaWarps * 32) + threadIdx.x; i < group * D; i += splits * (kMmaWarps * 32)) {
-        const int head = i / D, d = i % D;
-        float ms[kMaxSplits], ls[kMaxSplits], os[kMaxSplits];
-#pragma unroll
-        for (int c = 0; c < kMaxSplits; ++c) {
-            ms[c] = c < splits ? load_cluster(&c_m[head], c) : kNegInf;
-            ls[c] = c < splits ? load_cluster(&c_l[head], c) : 0.f;
-            os[c] = c < splits ? load_cluster(&s_o[0][head][d], c) : 0.f;
-        }
-        float top = kNegInf;
-#pragma unroll
-        for (int c = 0; c < kMaxSplits; ++c) top = fmaxf(top, ms[c]);
-        const float base = top == kNegInf ? 0.f : top;
-        float sum = 0.f, acc = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxSplits; ++c) {
-            const float weight = exp2f(ms[c] - base);
-            sum = fmaf(ls[c], weight, sum);
-            acc = fmaf(os[c], weight, acc);
-        }
-        store_out(p, (row * p.num_q_heads + h * group + head) * D + d, sum == 0.f ? 0.f : acc / sum);
-    }
-    cluster_sync();  // the shared memory lives until the cluster has read it
+    join_states<kSparseWarps, kHeads, D>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
 }
 
-template <int D, int NT>
-int launch_mma(const SparseParams& p, cudaStream_t st) {
-    constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB in flight a warp
-    constexpr size_t kSmem = (size_t)kMmaWarps * kStages * (D / 8) * 512;
-    static_assert(kSmem >= (size_t)kMmaWarps * NT * 8 * D * 4, "the states fit in the ring");
-    auto kernel = sparse_mma_kernel<D, NT, kStages>;
-    static std::atomic<unsigned long long> configured{0};
+// ---------------------------------------------------------------------------
+// fp32: CUDA cores
+// ---------------------------------------------------------------------------
+// D / 4 lanes hold a token's row, 4 channels each (one row of D 128, two of
+// D 64 side by side), through the same rings, a half-tile of 8 tokens a stage;
+// a lane reads back only what it copied.  Four tokens of a lane group at a
+// time: the products of 4 G scores are summed over the lanes by one
+// reduce-scatter (about 4 G shuffles instead of 4 G log2(D / 4)), so that each
+// weight is computed by one lane or few, and reaches the others through shared
+// memory.
+template <int D, int G, int kStages>
+__global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_f32_kernel(const SparseParams p, int splits) {
+    constexpr int kLanes = D / 4;
+    constexpr int kRows = 32 / kLanes;        // tokens side by side
+    constexpr int kOwn = 8 / kRows;           // tokens of a lane group in a half-tile
+    constexpr int kStage = 2 * 8 * D * 4;     // K and V of a half-tile
+    constexpr int kStates = kSparseWarps * kRows;
+    constexpr int kValues = 4 * G;            // scores of 4 tokens
+    constexpr int kHeld = kValues > kLanes ? kValues / kLanes : 1;  // of them in a lane
+    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][K, V][row][lane], later the states
+    __shared__ float s_m[kStates][G], s_l[kStates][G], c_m[G], c_l[G];
+    __shared__ __align__(16) float s_p[kSparseWarps][kRows][kValues];
+    const float kNegInf = __int_as_float(0xff800000);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = lane / kLanes, x = lane % kLanes;
+
+    const int per_block = p.block_size / 8;
+    const int shift = per_block == 1 ? 0 : per_block == 2 ? 1 : 2;
+    const int64_t halves = (int64_t)p.max_selected * per_block;
+    const int step = splits * kSparseWarps;
+    Row r;
+    r.rank = splits > 1 ? cluster_rank() : 0;
+    int64_t first = (int64_t)r.rank * kSparseWarps + warp;  // this warp's half-tiles, 32 at a time
+    int64_t half = first + (int64_t)lane * step;
+    int entry = r.open(p, splits, half, halves, shift);
+
+    const float* k_pool = static_cast<const float*>(p.k_pool) + sub * D + 4 * x;
+    const float* v_pool = static_cast<const float*>(p.v_pool) + sub * D + 4 * x;
+    uint8_t* mine = ring + warp * (kStages * kStage) + lane * 16;
+    float4 q[G], o[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        q[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                                (r.row * p.num_q_heads + r.h * G + i) * D + 4 * x);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // the lane's scores are values x * kValues / kLanes + i, of token value / G
+    // and head value % G; m and l are of those heads, l over its own tokens
+    const int value0 = x * kValues / kLanes;
+    float m[kHeld], l[kHeld] = {};
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) m[i] = kNegInf;
+
+    for (; first < halves && r.ok; first += (int64_t)step * 32) {
+        uint32_t at;
+        const int held = r.place(p, entry, (int)(half & (per_block - 1)), per_block, at);
+        half += (int64_t)step * 32;
+        entry = half < halves ? r.list[half >> shift] : -1;
+        unsigned todo = __ballot_sync(0xffffffffu, held > 0);
+
+        auto fetch = [&](int lead, int stage) {
+            const int left = __shfl_sync(0xffffffffu, held, lead) - sub;
+            const size_t off = (size_t)__shfl_sync(0xffffffffu, at, lead) * (8 * D);
+            const uint32_t dst = smem_addr(mine) + stage * kStage;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                copy_async16(dst + i * 512, k_pool + off + i * kRows * D, i * kRows < left);
+                copy_async16(dst + kStage / 2 + i * 512, v_pool + off + i * kRows * D, i * kRows < left);
+            }
+        };
+        unsigned ahead = todo;
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) {
+            if (ahead) fetch(__ffs(ahead) - 1, st);
+            ahead &= ahead - 1;
+            copy_async_commit();
+        }
+        for (int stage = 0; todo; todo &= todo - 1, stage = stage + 1 == kStages ? 0 : stage + 1) {
+            const int n = __shfl_sync(0xffffffffu, held, __ffs(todo) - 1);
+            copy_async_wait<kStages - 1>();
+            const float4* rows = reinterpret_cast<const float4*>(mine + stage * kStage);
+#pragma unroll
+            for (int t0 = 0; t0 < kOwn; t0 += 4) {
+                float s[kValues];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float4 k = rows[(t0 + t) * 32];
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        s[t * G + i] = fmaf(q[i].x, k.x, q[i].y * k.y) + fmaf(q[i].z, k.z, q[i].w * k.w);
+                }
+                reduce_scatter<kValues, kLanes>(s);
+                // as in the bf16 kernel, m moves only when a score passes it by 8
+                bool over = false;
+                float y[kHeld];
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const int t = (t0 + (value0 + i) / G) * kRows + sub;
+                    y[i] = t < n ? s[i] * p.scale_log2 : kNegInf;
+                    over |= y[i] > m[i] + 8.f;
+                }
+                if (__any_sync(0xffffffffu, over)) {
+                    float keep[kHeld];
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i) {
+                        float top = fmaxf(m[i], y[i]);  // over the four tokens
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, kLanes / 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, kLanes / 2));
+                        keep[i] = exp2_approx(m[i] - (top == kNegInf ? 0.f : top));
+                        m[i] = top;
+                        l[i] *= keep[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        const float w = __shfl_sync(0xffffffffu, keep[kHeld == 1 ? 0 : i % kHeld],
+                                                    kHeld == 1 ? i * kLanes / kValues : i / kHeld, kLanes);
+                        o[i].x *= w; o[i].y *= w; o[i].z *= w; o[i].w *= w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const float w = exp2_approx(y[i] - (m[i] == kNegInf ? 0.f : m[i]));
+                    l[i] += w;
+                    s_p[warp][sub][value0 + i] = w;  // the same from every lane that has it
+                }
+                __syncwarp();
+                float w[kValues];
+#pragma unroll
+                for (int i = 0; i < kValues; i += 4)
+                    *reinterpret_cast<float4*>(&w[i]) = *reinterpret_cast<const float4*>(&s_p[warp][sub][i]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float4 v = rows[kStage / 32 + (t0 + t) * 32];
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        o[i].x = fmaf(w[t * G + i], v.x, o[i].x);
+                        o[i].y = fmaf(w[t * G + i], v.y, o[i].y);
+                        o[i].z = fmaf(w[t * G + i], v.z, o[i].z);
+                        o[i].w = fmaf(w[t * G + i], v.w, o[i].w);
+                    }
+                }
+                __syncwarp();  // s_p is read
+            }
+            if (ahead) fetch(__ffs(ahead) - 1, stage);
+            ahead &= ahead - 1;
+            copy_async_commit();
+        }
+    }
+
+    copy_async_wait<0>();
+    __syncthreads();
+    float(*s_o)[G][D] = reinterpret_cast<float(*)[G][D]>(ring);
+    const int state = warp * kRows + sub;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], kLanes / 4);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], kLanes / 2);
+        if (x < kLanes / 4) {  // token 0's lanes
+            s_m[state][value0 + i] = m[i];
+            s_l[state][value0 + i] = l[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) *reinterpret_cast<float4*>(&s_o[state][i][4 * x]) = o[i];
+    join_states<kStates, G, D>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
+}
+
+// `step_tokens`: tokens that a warp takes at a time.
+int launch_sparse(const SparseParams& p, void (*kernel)(SparseParams, int), std::atomic<unsigned long long>& configured,
+                  size_t smem, int step_tokens, cudaStream_t st) {
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return PA_ERR_CUDA;
         configured.fetch_or(bit);
     }
@@ -514,17 +569,17 @@ int launch_mma(const SparseParams& p, cudaStream_t st) {
     // lists 15.6 against 17.8 and 21.3.  Below that, as many as give each SM
     // one (16 lists of 512 blocks: 72.8 us with one, 16.9 with eight); and three
     // an SM, which is what its shared memory holds, where each warp then still
-    // has 16 tiles (128 lists of 256 blocks: 49.3 us with one, 47.6 with three).
-    const int64_t tiles = ((int64_t)p.max_selected * p.block_size + 15) / 16;
+    // has 16 steps (128 lists of 256 blocks: 49.3 us with one, 47.6 with three).
+    const int64_t steps = ((int64_t)p.max_selected * p.block_size + step_tokens - 1) / step_tokens;
     const int64_t fill = num_sms() / units, hold = 3 * num_sms() / units;
-    int64_t splits = std::max(fill, std::min(hold, tiles / (kMmaWarps * 16)));
-    splits = std::min(splits, std::min((int64_t)kMaxSplits, (tiles + kMmaWarps - 1) / kMmaWarps));
+    int64_t splits = std::max(fill, std::min(hold, steps / (kSparseWarps * 16)));
+    splits = std::min(splits, std::min((int64_t)kMaxSplits, (steps + kSparseWarps - 1) / kSparseWarps));
     splits = std::max(splits, (int64_t)1);
-    if (units * splits > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    if (units > 0x7fffffff / splits) return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * splits));
-    cfg.blockDim = dim3(kMmaWarps * 32);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(kSparseWarps * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -540,6 +595,36 @@ int launch_mma(const SparseParams& p, cudaStream_t st) {
         return PA_ERR_CUDA;
     }
     return launch_status();
+}
+
+// Rings of 16 KB a warp, 64 KB a CTA, three CTAs an SM.
+constexpr size_t kRing = (size_t)kSparseWarps * 16384;
+
+template <int D, int NT>
+int launch_mma(const SparseParams& p, cudaStream_t st) {
+    constexpr int kStages = 16384 / (2 * 16 * 2 * D);
+    static_assert((size_t)kSparseWarps * NT * 8 * D * 4 <= kRing, "the states fit in the ring");
+    static std::atomic<unsigned long long> configured{0};
+    return launch_sparse(p, sparse_mma_kernel<D, NT, kStages>, configured, kRing, 16, st);
+}
+
+template <int D, int G>
+int launch_f32(const SparseParams& p, cudaStream_t st) {
+    constexpr int kStages = 16384 / (2 * 8 * 4 * D);
+    static_assert((size_t)kSparseWarps * (128 / D) * G * D * 4 <= kRing, "the states fit in the ring");
+    static std::atomic<unsigned long long> configured{0};
+    return launch_sparse(p, sparse_f32_kernel<D, G, kStages>, configured, kRing, 8, st);
+}
+
+template <int D>
+int launch_f32_group(const SparseParams& p, cudaStream_t st) {
+    switch (p.num_q_heads / p.num_kv_heads) {
+        case 1: return launch_f32<D, 1>(p, st);
+        case 2: return launch_f32<D, 2>(p, st);
+        case 4: return launch_f32<D, 4>(p, st);
+        case 8: return launch_f32<D, 8>(p, st);
+    }
+    return PA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -594,5 +679,5 @@ extern "C" int pa_paged_attention_decode_sparse(const void* q, const void* k_poo
             return head_dim == 128 ? launch_mma<128, 2>(p, st) : launch_mma<64, 2>(p, st);
         return head_dim == 128 ? launch_mma<128, 1>(p, st) : launch_mma<64, 1>(p, st);
     }
-    return head_dim == 128 ? launch_simt<float, 128>(p, st) : launch_simt<float, 64>(p, st);
+    return head_dim == 128 ? launch_f32_group<128>(p, st) : launch_f32_group<64>(p, st);
 }
