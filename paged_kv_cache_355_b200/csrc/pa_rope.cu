@@ -13,9 +13,9 @@
 // A row of D elements lies in D / 8 lanes, so a warp takes 2 (D 128) or 4 (D 64)
 // heads at a time and the norm's sum comes by shuffles.  One warp stays with
 // one token (or a slice of its heads), whose angles it gathers once into shared
-// memory, and keeps the rows after the ones it works on in flight.  Where the
-// whole head is rotated in halves, a lane holds 4 elements of each half, so
-// both elements of a pair; in part rotated ones the far half comes by shuffles.
+// memory, and keeps the rows after the ones it works on in flight.  A lane
+// holds 8 elements, both elements of four pairs: 8 neighbours, or 4 of each half
+// of the rotated part.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,12 +30,6 @@
 namespace pa {
 namespace {
 
-
-enum Pairing {
-    kNeighbours,  // (2p, 2p + 1)
-    kHalves,      // (p, p + rotary_dim / 2)
-    kWholeHalves  // the same, rotary_dim = head_dim
-};
 
 struct RopeParams {
     const void *query, *key, *value;
@@ -66,7 +60,7 @@ struct RopeParams {
 
 // One warp is one CTA, so that all that depends on its token and step alone is
 // the same for the whole CTA and stays off the lanes.
-template <typename T, int D, Pairing PAIRING, bool DECODE>
+template <typename T, int D, bool NEIGHBOURS, bool WHOLE, bool DECODE>  // WHOLE: rotary_dim is D
 __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) {
     constexpr int kLanes = D / kChunk;              // lanes of one head row
     constexpr int kHeads = 32 / kLanes;             // head rows of a step
@@ -78,9 +72,11 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     const int slice = (int)(blockIdx.x - token * p.slices);
     const int lane = threadIdx.x;
     const int sub = lane / kLanes, x = lane % kLanes;
-    // the lane's elements: 8 from `own`, or 4 there and 4 in the other half
-    const int own = PAIRING == kWholeHalves ? x * 4 : x * 8;
-    constexpr int kOther = PAIRING == kWholeHalves ? D / 2 : 4;
+    // the lane's elements: 4 from `own` and 4 from own + other; past the rotated
+    // part, or where neighbours pair, they follow one another
+    const bool turned = WHOLE || x * kChunk < p.rotary_dim;
+    const int own = NEIGHBOURS || !turned ? x * 8 : x * 4;
+    const int other = NEIGHBOURS || !turned ? 4 : WHOLE ? D / 2 : p.rotary_dim / 2;
 
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
     const int q_steps = (Hq + kHeads - 1) / kHeads, kv_steps = (Hkv + kHeads - 1) / kHeads;
@@ -98,7 +94,7 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
             const int head = (st < q_steps ? st : st < v_first ? st - q_steps : st - v_first) * kHeads;
             const T* src = (st < q_steps ? q_src : st < v_first ? k_src : v_src) + (int64_t)head * D;
             to[u] = Chunk<T>{};
-            if (st < end && head + sub < (st < q_steps ? Hq : Hkv)) to[u].load(src + src_lane, src + src_lane + kOther);
+            if (st < end && head + sub < (st < q_steps ? Hq : Hkv)) to[u].load(src + src_lane, src + src_lane + other);
         }
     };
     load(rows, first);  // beside the look-up of where they go
@@ -147,46 +143,29 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     if (!write) return;  // the same for every lane
     __syncwarp();        // the angles are in
 
-    // Coefficients of the lane's elements, weights multiplied in.  Both elements
-    // of a pair in the lane: (y1, y2) -> (y1 f[0] - y2 f[1], y2 f[2] + y1 f[3]),
-    // four pairs.  Across lanes (kHalves): y f[0..1] is the weighted row, f[2..3]
-    // cosines and f[4..5] signed sines, 8 elements each.
-    constexpr bool kInLane = PAIRING != kHalves;
-    const bool turned = PAIRING == kWholeHalves || x * kChunk < p.rotary_dim;
-    const int shift = p.rotary_dim / (2 * kChunk);  // kHalves: lanes between the elements of a pair
-    const bool second = PAIRING == kHalves && x >= shift;
-    const int partner = !turned ? lane : second ? lane - shift : lane + shift;
-    float f[kInLane ? 4 : 6][4];
+    // coefficients of the lane's four pairs, weights multiplied in:
+    // (y1, y2) -> (y1 f[0] - y2 f[1], y2 f[2] + y1 f[3])
+    float f[4][4];
     auto coefficients = [&](const void* weight) {
         float w[kChunk];
         if (weight) {
             Chunk<T> c;
-            c.load(static_cast<const T*>(weight) + own, static_cast<const T*>(weight) + own + kOther);
+            c.load(static_cast<const T*>(weight) + own, static_cast<const T*>(weight) + own + other);
             c.to_f32(w);
         } else {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) w[i] = 1.f;
         }
-        if (kInLane) {
-            const float4 a = turned ? *reinterpret_cast<const float4*>(&cs[0][x * 4]) : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float4 b = turned ? *reinterpret_cast<const float4*>(&cs[1][x * 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float c[4] = {a.x, a.y, a.z, a.w}, s[4] = {b.x, b.y, b.z, b.w};
+        const float4 a = turned ? *reinterpret_cast<const float4*>(&cs[0][x * 4]) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 b = turned ? *reinterpret_cast<const float4*>(&cs[1][x * 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float c[4] = {a.x, a.y, a.z, a.w}, s[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w1 = w[PAIRING == kWholeHalves ? i : 2 * i], w2 = w[PAIRING == kWholeHalves ? i + 4 : 2 * i + 1];
-                f[0][i] = w1 * c[i];
-                f[1][i] = w2 * s[i];
-                f[2][i] = w2 * c[i];
-                f[3][i] = w1 * s[i];
-            }
-        } else {
-            const int at = turned ? (second ? x - shift : x) * 8 : 0;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                f[i / 4][i % 4] = w[i];
-                f[kInLane ? 0 : 2 + i / 4][i % 4] = cs[0][at + i];
-                f[kInLane ? 0 : 4 + i / 4][i % 4] = second ? cs[1][at + i] : -cs[1][at + i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float w1 = w[NEIGHBOURS ? 2 * i : i], w2 = w[NEIGHBOURS ? 2 * i + 1 : i + 4];
+            f[0][i] = w1 * c[i];
+            f[1][i] = w2 * s[i];
+            f[2][i] = w2 * c[i];
+            f[3][i] = w1 * s[i];
         }
     };
     const int64_t blk = slot / p.block_size;
@@ -221,32 +200,23 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) y[i] *= inv;
                 }
-                if (kInLane) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int a = PAIRING == kWholeHalves ? i : 2 * i, b = PAIRING == kWholeHalves ? i + 4 : 2 * i + 1;
-                        const float y1 = y[a], y2 = y[b];
-                        if (turned) {
-                            y[a] = fmaf(y1, f[0][i], -(y2 * f[1][i]));
-                            y[b] = fmaf(y2, f[2][i], y1 * f[3][i]);
-                        } else {
-                            y[a] = y1 * f[0][i];
-                            y[b] = y2 * f[2][i];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        y[i] *= f[i / 4][i % 4];
-                        const float z = __shfl_sync(0xffffffffu, y[i], partner);
-                        if (turned) y[i] = fmaf(y[i], f[kInLane ? 0 : 2 + i / 4][i % 4], z * f[kInLane ? 0 : 4 + i / 4][i % 4]);
+                for (int i = 0; i < 4; ++i) {
+                    const int a = NEIGHBOURS ? 2 * i : i, b = NEIGHBOURS ? 2 * i + 1 : i + 4;
+                    const float y1 = y[a], y2 = y[b];
+                    if (turned) {
+                        y[a] = fmaf(y1, f[0][i], -(y2 * f[1][i]));
+                        y[b] = fmaf(y2, f[2][i], y1 * f[3][i]);
+                    } else {  // not by a sine of 0: the other element may be infinite
+                        y[a] = y1 * f[0][i];
+                        y[b] = y2 * f[2][i];
                     }
                 }
                 rows[u].from_f32(y);
             }
             T* dst = is_q ? q_dst + (int64_t)head * D + src_lane
                           : (is_v ? v_dst : k_dst) + head * head_stride + pool_lane;
-            if (head + sub < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + kOther);
+            if (head + sub < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + other);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) rows[u] = next[u];
@@ -266,14 +236,15 @@ int launch_rope(RopeParams p, bool interleaved, cudaStream_t stream) {
     const int64_t all = steps * p.num_tokens, sms = num_sms();
     int64_t per_warp = all / (sms * 64);
     if (per_warp < 4 && all >= sms * 32) per_warp = 4;
+    if (per_warp < 16 && p.num_tokens * ((steps + 15) / 16) >= sms * 28) per_warp = 16;
     per_warp = std::max((int64_t)1, std::min(per_warp, steps));
     p.slices = (int)((steps + per_warp - 1) / per_warp);
     p.steps = (int)((steps + p.slices - 1) / p.slices);  // evened out
     const int64_t blocks = p.num_tokens * p.slices;
     if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    auto kernel = interleaved            ? rope_cache_kernel<T, D, kNeighbours, DECODE>
-                  : p.rotary_dim == D    ? rope_cache_kernel<T, D, kWholeHalves, DECODE>
-                                         : rope_cache_kernel<T, D, kHalves, DECODE>;
+    const bool whole = p.rotary_dim == D;
+    auto kernel = interleaved ? (whole ? rope_cache_kernel<T, D, true, true, DECODE> : rope_cache_kernel<T, D, true, false, DECODE>)
+                              : (whole ? rope_cache_kernel<T, D, false, true, DECODE> : rope_cache_kernel<T, D, false, false, DECODE>);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32), 0, stream, p);
 }
 

@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <atomic>
@@ -42,7 +43,7 @@ struct BoundsParams {
     int* err;
 };
 
-// The running minimum and maximum of a lane's 8 channels, NaN kept.
+// The running minimum and maximum of a lane's 16 bytes of channels, NaN kept.
 template <typename T>
 struct Range;
 
@@ -67,8 +68,8 @@ struct Range<__nv_bfloat16> {
             hi[i] = 0xff80ff80u;
         }
     }
-    __device__ __forceinline__ void take(const Chunk<__nv_bfloat16>& c) {
-        const uint32_t x[4] = {c.a.x, c.a.y, c.a.z, c.a.w};
+    __device__ __forceinline__ void take(const uint4& c) {
+        const uint32_t x[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             lo[i] = min2_nan(lo[i], x[i]);
@@ -90,37 +91,32 @@ struct Range<__nv_bfloat16> {
 
 template <>
 struct Range<float> {
-    float lo[8], hi[8];
+    float lo[4], hi[4];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             lo[i] = __int_as_float(0x7f800000);
             hi[i] = __int_as_float(0xff800000);
         }
     }
-    __device__ __forceinline__ void take(const Chunk<float>& c) {
-        float x[kChunk];
-        c.to_f32(x);
+    __device__ __forceinline__ void take(const uint4& c) {
+        const uint32_t x[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo[i] = min_nan(lo[i], x[i]);
-            hi[i] = max_nan(hi[i], x[i]);
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = min_nan(lo[i], __uint_as_float(x[i]));
+            hi[i] = max_nan(hi[i], __uint_as_float(x[i]));
         }
     }
     __device__ __forceinline__ void join(int lanes) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], lanes));
             hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], lanes));
         }
     }
     __device__ __forceinline__ void store(float* p, bool high) const {
-        Chunk<float> c;
-        float x[kChunk];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = high ? hi[i] : lo[i];
-        c.from_f32(x);
-        c.store(p);
+        *reinterpret_cast<float4*>(p) =
+            high ? make_float4(hi[0], hi[1], hi[2], hi[3]) : make_float4(lo[0], lo[1], lo[2], lo[3]);
     }
 };
 
@@ -136,14 +132,13 @@ constexpr int kPieceBytes = 4096;
 
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsParams p) {
-    constexpr int kLanes = D / kChunk;
+    constexpr int kElems = 16 / sizeof(T);                    // channels of a lane
+    constexpr int kLanes = D / kElems;                        // lanes of one row
     constexpr int kRows = 32 / kLanes;                        // rows side by side
     constexpr int kOwn = BS / kRows;                          // rows of one lane
-    constexpr int kMost = kPieceBytes / (32 * kChunk * (int)sizeof(T));  // of a piece
-    constexpr int kBatch = kOwn < kMost ? kOwn : kMost;
+    constexpr int kBatch = kOwn < kPieceBytes / 512 ? kOwn : kPieceBytes / 512;  // of a piece
     constexpr int kPerHead = kOwn / kBatch;                   // pieces of one head
-    constexpr int kVec = kChunk * sizeof(T) / 16;             // 16-byte vectors of a chunk
-    extern __shared__ __align__(16) uint8_t ring[];           // [warp][piece][row][vector][lane]
+    extern __shared__ __align__(16) uint8_t ring[];           // [warp][piece][row][lane]
     griddep_wait();
     griddep_launch_dependents();
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -176,8 +171,8 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
     const int held = left < BS ? (int)left : BS;  // tokens of the block
     const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, p.num_kv_heads);
     const int64_t row = blk * p.num_kv_heads + h0;
-    const T* src = static_cast<const T*>(p.k_pool) + row * (BS * D) + sub * D + chunk * kChunk;
-    T* dst = static_cast<T*>(p.key_bounds) + row * (2 * D) + (sub & 1) * D + chunk * kChunk;
+    const T* src = static_cast<const T*>(p.k_pool) + row * (BS * D) + sub * D + chunk * kElems;
+    T* dst = static_cast<T*>(p.key_bounds) + row * (2 * D) + (sub & 1) * D + chunk * kElems;
     uint8_t* mine = ring + (threadIdx.x >> 5) * (kPieces * kPieceBytes) + lane * 16;
 
     const int pieces = (h1 - h0) * kPerHead;
@@ -188,10 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
             const uint32_t to = smem_addr(mine) + fetched % kPieces * kPieceBytes;
 #pragma unroll
             for (int t = 0; t < kBatch; ++t)
-#pragma unroll
-                for (int v = 0; v < kVec; ++v)
-                    copy_async16(to + (t * kVec + v) * 512, src + (t0 + t) * kRows * D + v * (16 / sizeof(T)),
-                                 (t0 + t) * kRows + sub < held);
+                copy_async16(to + t * 512, src + (t0 + t) * kRows * D, (t0 + t) * kRows + sub < held);
             ++fetched;
             if (fetched % kPerHead == 0) src += BS * D;
         }
@@ -205,11 +197,9 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
         if (kPerHead == 1 || done % kPerHead == 0) r.clear();
         const int t0 = done % kPerHead * kBatch;
         const uint8_t* from = mine + done % kPieces * kPieceBytes;
-        Chunk<T> rows[kBatch];
+        uint4 rows[kBatch];
 #pragma unroll
-        for (int t = 0; t < kBatch; ++t)
-            rows[t].load(reinterpret_cast<const T*>(from + t * kVec * 512),
-                         reinterpret_cast<const T*>(from + t * kVec * 512 + (kVec == 2 ? 512 : 8)));
+        for (int t = 0; t < kBatch; ++t) rows[t] = *reinterpret_cast<const uint4*>(from + t * 512);
 #pragma unroll
         for (int t = 0; t < kBatch; ++t)
             if ((t0 + t) * kRows + sub < held) r.take(rows[t]);
@@ -217,7 +207,12 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
         if (kPerHead == 1 || (done + 1) % kPerHead == 0) {
 #pragma unroll
             for (int m = kLanes; m < 32; m <<= 1) r.join(m);
-            if (sub < 2) r.store(dst, sub == 1);
+            if (kRows == 1) {
+                r.store(dst, false);
+                r.store(dst + D, true);
+            } else if (sub < 2) {
+                r.store(dst, sub == 1);
+            }
             dst += 2 * D;
         }
     }
@@ -264,28 +259,32 @@ struct ScoreParams {
     int64_t num_rows;
     int num_q_heads, num_kv_heads;
     int64_t num_blocks;
-    int chunks, tiles_per_warp;  // CTAs of one (row, kv head); tiles of 16 blocks of one warp
+    // a warp takes heads_per_warp kv heads of tiles_per_warp tiles of 16 blocks of
+    // a row: `parts` of the heads and `chunks` of the tiles are CTAs of their own
+    int heads_per_warp, tiles_per_warp, parts, chunks;
     int* err;
 };
 
-// This warp's part of a (row, kv head): `tiles_per_warp` tiles of 16 blocks,
-// every kWarps-th, so that a short row still occupies all warps.
+// This warp's part of a row: `tiles_per_warp` tiles of 16 blocks, every
+// kWarps-th, so that a short row still occupies all warps, and some kv heads.
 struct WarpTiles {
     const int32_t* table;
-    int64_t unit;  // row * num_kv_heads + kv head
-    int h, blocks, first, end;
-    bool named;    // the row's sequence exists
+    int64_t row;
+    int h0, heads, blocks, first, end;
+    bool named, recorder;  // the row's sequence exists; this thread reports a bad row
 };
 
 // Where the warp is, without the row's length: its table may be read beside it.
 __device__ __forceinline__ WarpTiles warp_tiles(const ScoreParams& p) {
     WarpTiles w;
-    w.unit = blockIdx.x / p.chunks;
-    const int chunk = (int)(blockIdx.x - w.unit * p.chunks);
-    const int64_t row = w.unit / p.num_kv_heads;
-    w.h = (int)(w.unit - row * p.num_kv_heads);
-    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[row] : row;
+    const int64_t unit = blockIdx.x / p.chunks;
+    const int chunk = (int)(blockIdx.x - unit * p.chunks);
+    w.row = unit / p.parts;
+    w.h0 = (int)(unit - w.row * p.parts) * p.heads_per_warp;
+    w.heads = min(p.heads_per_warp, p.num_kv_heads - w.h0);
+    const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[w.row] : w.row;
     w.named = seq >= 0 && seq < p.batch;
+    w.recorder = chunk == 0 && w.h0 == 0 && threadIdx.x == 0;
     w.table = p.block_tables + (w.named ? seq : 0) * p.max_blocks_per_seq;
     w.first = chunk * kWarps * p.tiles_per_warp + (threadIdx.x >> 5);
     w.end = w.first + kWarps * p.tiles_per_warp;
@@ -300,9 +299,9 @@ __device__ __forceinline__ int32_t entry_of(const ScoreParams& p, const WarpTile
 
 // The row's length, which ends the warp's tiles.
 __device__ __forceinline__ void end_tiles(const ScoreParams& p, WarpTiles& w) {
-    const int L = p.context_lens[w.unit / p.num_kv_heads];
+    const int L = p.context_lens[w.row];
     if (!w.named || L < 0 || L > p.max_context_len) {
-        if (blockIdx.x % p.chunks == 0 && w.h == 0 && threadIdx.x == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
+        if (w.recorder) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
     } else {
         w.blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
     }
@@ -320,6 +319,40 @@ __device__ __forceinline__ int32_t block_of(const ScoreParams& p, const WarpTile
     return entry;
 }
 
+// The table entries of a warp's tiles, looked up two tiles (a pair) at a time:
+// lane i holds block i % 16 of tile 2 * pair + i / 16 of the warp's sequence,
+// e0 of the pair being scored, e1 of the next one, which is being fetched.
+struct Entries {
+    int32_t e0, e1;
+    int j, last, pair;
+    static constexpr int kPair = 2 * kWarps * 16;  // blocks between a lane's blocks of two pairs
+
+    // Reads beside the row's length; false where the warp has no tile.
+    __device__ __forceinline__ bool open(const ScoreParams& p, WarpTiles& w) {
+        const int lane = threadIdx.x & 31;
+        j = (w.first + (lane >> 4) * kWarps) * 16 + (lane & 15);
+        e0 = entry_of(p, w, j);
+        e1 = entry_of(p, w, j + kPair);
+        end_tiles(p, w);
+        if (w.first >= w.end) return false;
+        last = w.end * 16;  // blocks of other CTAs lie behind
+        e0 = j < last ? block_of(p, w, j, e0) : -1;
+        j += kPair;
+        e1 = j < last ? block_of(p, w, j, e1) : -1;
+        pair = 0;
+        return true;
+    }
+    __device__ __forceinline__ int32_t at(int tile, int block) const {  // of the warp's sequence
+        return __shfl_sync(0xffffffffu, (tile >> 1) == pair ? e0 : e1, (tile & 1) * 16 + block);
+    }
+    __device__ __forceinline__ void next_pair(const ScoreParams& p, const WarpTiles& w) {
+        ++pair;
+        e0 = e1;
+        j += kPair;
+        e1 = j < last ? block_of(p, w, j, entry_of(p, w, j)) : -1;
+    }
+};
+
 // bf16.  max(q lo, q hi) is q hi where q >= 0 and q lo where q < 0, so a score
 // is the dot product of (q-, q+) with (lo, hi) over 2 D terms, all of whose
 // products are exact: a matrix product (m16n8k16) of 16 blocks with the group's
@@ -328,7 +361,8 @@ __device__ __forceinline__ int32_t block_of(const ScoreParams& p, const WarpTile
 // asynchronously into a ring of two tiles that belongs to the warp alone.
 // 16-byte chunk c of block b lies at c ^ (b & 7), so that the eight rows of a
 // matrix load touch all banks.
-template <int D, int NT>
+// HEADS: the warp goes through several kv heads of each tile and reloads q.
+template <int D, int NT, bool HEADS>
 __global__ void __launch_bounds__(kWarps * 32, 3) block_scores_mma_kernel(const ScoreParams p) {
     constexpr int kRowBytes = 4 * D;            // lo and hi of one block
     constexpr int kTile = 16 * kRowBytes;
@@ -339,155 +373,206 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block_scores_mma_kernel(const 
     griddep_wait();
     griddep_launch_dependents();
     WarpTiles w = warp_tiles(p);
+    Entries e;
+    if (!e.open(p, w)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    // lane i: block i of a pair of tiles; e0 of the pair being multiplied, e1 of
-    // the one being fetched
-    int j = (w.first + (lane >> 4) * kWarps) * 16 + (lane & 15);
-    constexpr int kPair = 2 * kWarps * 16;  // blocks between a lane's blocks of two pairs
-    int32_t e0 = entry_of(p, w, j), e1 = entry_of(p, w, j + kPair);
-    end_tiles(p, w);
-    if (w.first >= w.end) return;
-    const int last = w.end * 16;  // blocks of other CTAs lie behind
-    e0 = j < last ? block_of(p, w, j, e0) : -1;
-    j += kPair;
-    e1 = j < last ? block_of(p, w, j, e1) : -1;
+    const int heads = HEADS ? w.heads : 1;
+    const int tiles = (w.end - w.first + kWarps - 1) / kWarps;
 
-    const int64_t row = w.unit / p.num_kv_heads;
     const int group = p.num_q_heads / p.num_kv_heads;
     const int copy_row = lane / kRowLanes, copy_chunk = lane % kRowLanes;
-    const __nv_bfloat16* bounds = static_cast<const __nv_bfloat16*>(p.key_bounds) + (int64_t)w.h * 2 * D + 8 * copy_chunk;
+    const __nv_bfloat16* bounds = static_cast<const __nv_bfloat16*>(p.key_bounds) + (int64_t)w.h0 * 2 * D + 8 * copy_chunk;
     const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
     const uint32_t slots = smem_addr(ring) + warp * (2 * kTile);
     const uint32_t copy_dst = slots + copy_row * kRowBytes;
-    auto fetch = [&](int32_t e, int half, int stage) {  // one tile: lanes 16 half .. of e
+    int f_tile = 0, f_head = 0;  // the next to be fetched
+    auto fetch = [&](int stage) {
+        if (f_tile < tiles) {
+            const __nv_bfloat16* src = bounds + f_head * (2 * D);
 #pragma unroll
-        for (int u = 0; u < 16; u += kCopyRows) {
-            const int32_t blk = __shfl_sync(0xffffffffu, e, 16 * half + u + copy_row);
-            const uint32_t dst = copy_dst + stage * kTile + u * kRowBytes + ((copy_chunk ^ ((u + copy_row) & 7)) << 4);
-            copy_async16(dst, bounds + (blk < 0 ? 0 : blk) * block_stride, blk >= 0);
+            for (int u = 0; u < 16; u += kCopyRows) {
+                const int32_t blk = e.at(f_tile, u + copy_row);
+                const uint32_t dst = copy_dst + stage * kTile + u * kRowBytes + ((copy_chunk ^ ((u + copy_row) & 7)) << 4);
+                copy_async16(dst, src + (blk < 0 ? 0 : blk) * block_stride, blk >= 0);
+            }
+            if (++f_head == heads) {
+                f_head = 0;
+                ++f_tile;
+            }
+        }
+        copy_async_commit();
+    };
+    fetch(0);
+    fetch(1);
+
+    // column 8 n + g of Q^T; its negative values (side 0) meet lo, the others hi
+    uint32_t q[HEADS ? 1 : 2][NT][kSteps][2];
+    auto part = [](uint32_t x, int side) {
+        uint32_t neg;  // the sign of each half, all over it
+        asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(x));
+        return side ? x & ~neg : x & neg;
+    };
+    auto load_q = [&](int head) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                       (w.row * p.num_q_heads + (w.h0 + head) * group + (8 * n + g) % group) * D + 2 * t;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c);
+                    if (HEADS) {
+                        q[0][n][i][c] = x;
+                    } else {
+                        q[0][n][i][c] = part(x, 0);
+                        q[HEADS ? 0 : 1][n][i][c] = part(x, 1);
+                    }
+                }
         }
     };
-    fetch(e0, 0, 0);
-    copy_async_commit();
-    if (w.first + kWarps < w.end) fetch(e0, 1, 1);
-    copy_async_commit();
-
-    uint32_t q[2][NT][kSteps][2];  // negative and other values of head 8 n + g
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int head = w.h * group + (8 * n + g) % group;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (row * p.num_q_heads + head) * D + 2 * t;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c);
-                uint32_t neg;  // the sign of each half, all over it
-                asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(x));
-                q[0][n][i][c] = x & neg;
-                q[1][n][i][c] = x & ~neg;
-            }
-    }
+    load_q(0);
     // matrix loads: lane = (matrix, row), the matrices (8 blocks, chunk of 8 channels)
     const uint32_t mat_row = lane & 7, mat_lo = (lane >> 3) & 1, mat_hi = lane >> 4;
     const uint32_t mat = slots + (mat_lo * 8 + mat_row) * kRowBytes + ((mat_hi ^ mat_row) << 4);
-    float* out = p.scores + w.unit * p.score_stride;
-    int half = 0;
-    for (int tile = w.first; tile < w.end; tile += kWarps, half ^= 1) {
-        copy_async_wait<1>();
-        __syncwarp();  // every lane's copies are in
-        float s[2][NT][4] = {};
+    int stage = 0;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const unsigned have = __ballot_sync(0xffffffffu, e.e0 >= 0) >> (16 * (tile & 1));
+        for (int head = 0; head < heads; ++head, stage ^= 1) {
+            copy_async_wait<1>();
+            __syncwarp();  // every lane's copies are in
+            float s[2][NT][4] = {};
 #pragma unroll
-        for (int side = 0; side < 2; ++side)
+            for (int side = 0; side < 2; ++side)
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                uint32_t a[4];
-                ldmatrix_x4((mat ^ (i << 5)) + half * kTile + side * 2 * D, a[0], a[1], a[2], a[3]);
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t a[4];
+                    ldmatrix_x4((mat ^ (i << 5)) + stage * kTile + side * 2 * D, a[0], a[1], a[2], a[3]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[side][n], a, q[side][n][i][0], q[side][n][i][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        if (HEADS)
+                            mma_bf16_16816(s[side][n], a, part(q[0][n][i][0], side), part(q[0][n][i][1], side));
+                        else
+                            mma_bf16_16816(s[side][n], a, q[HEADS ? 0 : side][n][i][0], q[HEADS ? 0 : side][n][i][1]);
+                    }
+                }
+            __syncwarp();  // every lane has read the stage
+            fetch(stage);
+            if (HEADS) load_q(head + 1 == heads ? 0 : head + 1);
+            // heads 2 t, 2 t + 1 (+ 8) of blocks g and g + 8
+            float* out = p.scores + (w.row * p.num_kv_heads + w.h0 + head) * p.score_stride + (w.first + tile * kWarps) * 16;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                float best = max_nan(s[0][0][2 * a] + s[1][0][2 * a], s[0][0][2 * a + 1] + s[1][0][2 * a + 1]);
+                if (NT == 2)
+                    best = max_nan(best, max_nan(s[0][NT - 1][2 * a] + s[1][NT - 1][2 * a],
+                                                 s[0][NT - 1][2 * a + 1] + s[1][NT - 1][2 * a + 1]));
+                best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 1));
+                best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 2));
+                if (t == a && (have >> (g + 8 * a) & 1)) out[g + 8 * a] = best;
             }
-        __syncwarp();  // every lane has read the stage
-        const unsigned have = __ballot_sync(0xffffffffu, e0 >= 0) >> (16 * half);
-        if (tile + 2 * kWarps < w.end) fetch(e1, half, half);
-        copy_async_commit();
-        if (half == 1) {
-            e0 = e1;
-            j += kPair;
-            e1 = j < last ? block_of(p, w, j, entry_of(p, w, j)) : -1;
         }
-        // heads 2 t, 2 t + 1 (+ 8) of blocks g and g + 8
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            float best = max_nan(s[0][0][2 * a] + s[1][0][2 * a], s[0][0][2 * a + 1] + s[1][0][2 * a + 1]);
-            if (NT == 2)
-                best = max_nan(best, max_nan(s[0][NT - 1][2 * a] + s[1][NT - 1][2 * a],
-                                             s[0][NT - 1][2 * a + 1] + s[1][NT - 1][2 * a + 1]));
-            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 1));
-            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 2));
-            if (t == a && (have >> (g + 8 * a) & 1)) out[tile * 16 + g + 8 * a] = best;
-        }
+        if (tile & 1) e.next_pair(p, w);
     }
     copy_async_wait<0>();
 }
 
 // fp32, on the CUDA cores: D / 4 lanes hold the two rows of a block, four
-// channels each, four blocks at a time; their sums over the lanes by one
-// reduce-scatter.
+// channels each, four blocks of a lane group at a time, through a ring of four
+// such pieces (a lane reads back only what it copied); their sums over the
+// lanes by one reduce-scatter.
 template <int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) block_scores_f32_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) block_scores_f32_kernel(const ScoreParams p) {
     constexpr int kLanes = D / 4;
-    constexpr int kRows = 32 / kLanes;    // blocks side by side
-    constexpr int kBlocks = 4;            // blocks of one lane
+    constexpr int kRows = 32 / kLanes;        // blocks side by side
+    constexpr int kBlocks = 4;                // of one lane in a piece
+    constexpr int kPiece = kBlocks * 2 * 512;
+    constexpr int kPerTile = 16 / (kBlocks * kRows);
+    constexpr int kStages = 4;
+    constexpr int kHeld = kBlocks * G > kLanes ? kBlocks * G / kLanes : 1;  // sums in a lane
+    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][block][lo, hi][lane]
     griddep_wait();
     griddep_launch_dependents();
     WarpTiles w = warp_tiles(p);
-    end_tiles(p, w);
-    if (w.first >= w.end) return;
+    Entries e;
+    if (!e.open(p, w)) return;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, x = lane % kLanes;
-    const int64_t row = w.unit / p.num_kv_heads;
-    float4 q[G];
-#pragma unroll
-    for (int i = 0; i < G; ++i)
-        q[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
-                                                (row * p.num_q_heads + w.h * G + i) * D + 4 * x);
-    const float* bounds = static_cast<const float*>(p.key_bounds) + (int64_t)w.h * 2 * D + 4 * x;
+    const int tiles = (w.end - w.first + kWarps - 1) / kWarps;
+    float4 neg[G], pos[G];  // q's negative values, which meet lo, and the others
+    const float* bounds = static_cast<const float*>(p.key_bounds) + (int64_t)w.h0 * 2 * D + 4 * x;
     const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
-    float* out = p.scores + w.unit * p.score_stride;
-    for (int tile = w.first; tile < w.end; tile += kWarps) {
-        for (int j0 = tile * 16 + sub; j0 < tile * 16 + 16; j0 += kBlocks * kRows) {
-            float4 lo[kBlocks], hi[kBlocks];
-            bool have[kBlocks];
+    uint8_t* mine = ring + (threadIdx.x >> 5) * (kStages * kPiece) + lane * 16;
+    int f_tile = 0, f_head = 0, f_part = 0;
+    auto fetch = [&](int stage) {
+        if (f_tile < tiles) {
+            const uint32_t dst = smem_addr(mine) + stage * kPiece;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
-                const int j = j0 + b * kRows;
-                const int32_t blk = block_of(p, w, j, entry_of(p, w, j));
-                have[b] = blk >= 0;
-                lo[b] = hi[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (have[b]) {
-                    lo[b] = *reinterpret_cast<const float4*>(bounds + blk * block_stride);
-                    hi[b] = *reinterpret_cast<const float4*>(bounds + blk * block_stride + D);
+                const int32_t blk = e.at(f_tile, (f_part * kBlocks + b) * kRows + sub);
+                const float* src = bounds + f_head * (2 * D) + (blk < 0 ? 0 : blk) * block_stride;
+                copy_async16(dst + b * 1024, src, blk >= 0);
+                copy_async16(dst + b * 1024 + 512, src + D, blk >= 0);
+            }
+            if (++f_part == kPerTile) {
+                f_part = 0;
+                if (++f_head == w.heads) {
+                    f_head = 0;
+                    ++f_tile;
                 }
             }
-            float v[kBlocks * G];
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-                    v[b * G + i] = q[i].x * (q[i].x < 0.f ? lo[b].x : hi[b].x) + q[i].y * (q[i].y < 0.f ? lo[b].y : hi[b].y) +
-                                   (q[i].z * (q[i].z < 0.f ? lo[b].z : hi[b].z) + q[i].w * (q[i].w < 0.f ? lo[b].w : hi[b].w));
-            reduce_scatter<kBlocks * G, kLanes>(v);
-            // lane x holds heads of block x / (kLanes / kBlocks)
-            float best = v[0];
-            constexpr int kHeld = kBlocks * G > kLanes ? kBlocks * G / kLanes : 1;
-#pragma unroll
-            for (int i = 1; i < kHeld; ++i) best = max_nan(best, v[i]);
-#pragma unroll
-            for (int m = kLanes / kBlocks / 2; m; m >>= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, m));
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-                if (x == b * (kLanes / kBlocks) && have[b]) out[j0 + b * kRows] = best;
         }
+        copy_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) fetch(st);
+    int stage = 0;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const unsigned have = __ballot_sync(0xffffffffu, e.e0 >= 0) >> (16 * (tile & 1));
+        for (int head = 0; head < w.heads; ++head) {
+            if (tile == 0 || w.heads > 1) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    const float4 q = *reinterpret_cast<const float4*>(
+                        static_cast<const float*>(p.q) + (w.row * p.num_q_heads + (w.h0 + head) * G + i) * D + 4 * x);
+                    neg[i] = make_float4(q.x < 0.f ? q.x : 0.f, q.y < 0.f ? q.y : 0.f, q.z < 0.f ? q.z : 0.f, q.w < 0.f ? q.w : 0.f);
+                    pos[i] = make_float4(q.x < 0.f ? 0.f : q.x, q.y < 0.f ? 0.f : q.y, q.z < 0.f ? 0.f : q.z, q.w < 0.f ? 0.f : q.w);
+                }
+            }
+            float* out = p.scores + (w.row * p.num_kv_heads + w.h0 + head) * p.score_stride + (w.first + tile * kWarps) * 16;
+            for (int part = 0; part < kPerTile; ++part, stage = (stage + 1) % kStages) {
+                copy_async_wait<kStages - 1>();
+                const float4* rows = reinterpret_cast<const float4*>(mine + stage * kPiece);
+                float v[kBlocks * G];
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const float4 lo = rows[b * 64], hi = rows[b * 64 + 32];
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        float a = neg[i].x * lo.x, c = pos[i].x * hi.x;
+                        a = fmaf(neg[i].y, lo.y, a);
+                        c = fmaf(pos[i].y, hi.y, c);
+                        a = fmaf(neg[i].z, lo.z, a);
+                        c = fmaf(pos[i].z, hi.z, c);
+                        a = fmaf(neg[i].w, lo.w, a);
+                        c = fmaf(pos[i].w, hi.w, c);
+                        v[b * G + i] = a + c;
+                    }
+                }
+                fetch(stage);
+                reduce_scatter<kBlocks * G, kLanes>(v);
+                // lane x holds heads of block x / (kLanes / kBlocks)
+                float best = v[0];
+#pragma unroll
+                for (int i = 1; i < kHeld; ++i) best = max_nan(best, v[i]);
+#pragma unroll
+                for (int m = kLanes / kBlocks / 2; m; m >>= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, m));
+                const int block = (part * kBlocks + x / (kLanes / kBlocks)) * kRows + sub;
+                if (x % (kLanes / kBlocks) == 0 && (have >> block & 1)) out[block] = best;
+            }
+        }
+        if (tile & 1) e.next_pair(p, w);
     }
+    copy_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -752,43 +837,61 @@ __global__ void __launch_bounds__(THREADS) select_long_kernel(const SelectParams
     }
 }
 
-template <int D, int NT>
-int launch_scores_mma(const ScoreParams& p, dim3 grid, cudaStream_t st) {
-    constexpr int kSmem = kWarps * 2 * 16 * 4 * D;
-    auto kernel = block_scores_mma_kernel<D, NT>;
-    static std::atomic<unsigned long long> configured{0};
+constexpr int kScoresSmem = kWarps * 16384;  // rings of 16 KB a warp (8 KB for bf16 of D 64)
+
+int launch_scores_kernel(const ScoreParams& p, void (*kernel)(ScoreParams), std::atomic<unsigned long long>& configured,
+                         int smem, cudaStream_t st) {
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return PA_ERR_CUDA;
         configured.fetch_or(bit);
     }
-    return launch_pdl(kernel, grid, dim3(kWarps * 32), kSmem, st, p);
+    const int64_t grid = p.num_rows * p.parts;
+    if (grid > 0x7fffffff / p.chunks) return PA_ERR_UNSUPPORTED;
+    return launch_pdl(kernel, dim3((unsigned)(grid * p.chunks)), dim3(kWarps * 32), smem, st, p);
+}
+
+template <int D, int NT>
+int launch_scores_mma(const ScoreParams& p, cudaStream_t st) {
+    constexpr int kSmem = kWarps * 2 * 16 * 4 * D;
+    static std::atomic<unsigned long long> one{0}, several{0};
+    return p.heads_per_warp > 1 ? launch_scores_kernel(p, block_scores_mma_kernel<D, NT, true>, several, kSmem, st)
+                                : launch_scores_kernel(p, block_scores_mma_kernel<D, NT, false>, one, kSmem, st);
+}
+
+template <int D, int G>
+int launch_scores_f32(const ScoreParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> configured{0};
+    return launch_scores_kernel(p, block_scores_f32_kernel<D, G>, configured, kScoresSmem, st);
 }
 
 int launch_scores(ScoreParams p, int head_dim, int dtype, cudaStream_t st) {
-    // tiles of 16 blocks of one warp: one while the grid is short of 8 warps an
-    // SM, up to 8 once it is not
-    const int64_t units = p.num_rows * p.num_kv_heads;
     const int64_t tiles = ((int64_t)p.max_context_len + 16 * p.block_size - 1) / (16 * p.block_size);
-    p.tiles_per_warp = (int)std::max((int64_t)1, std::min((int64_t)8, units * tiles / ((int64_t)num_sms() * 32)));
+    const int64_t all = p.num_rows * p.num_kv_heads * tiles, sms = num_sms();
+    // Rows of at most four tiles a warp: most of a ragged batch has far fewer,
+    // so what a warp gets more of is heads, of one tile, whose look-ups they
+    // share.  Longer rows: tiles of one head, up to 8 once the grid has 32 warps
+    // an SM.
+    const char* f = getenv("PA_NH");
+    const int64_t heads = tiles > 4 * kWarps ? 1 : std::max((int64_t)1, std::min((int64_t)p.num_kv_heads, f ? atoi(f) : all / (sms * 24)));
+    p.parts = (int)((p.num_kv_heads + heads - 1) / heads);
+    p.heads_per_warp = (p.num_kv_heads + p.parts - 1) / p.parts;
+    p.tiles_per_warp = p.heads_per_warp > 1 ? 1 : (int)std::max((int64_t)1, std::min((int64_t)8, all / (sms * 32)));
     p.chunks = (int)((tiles + kWarps * p.tiles_per_warp - 1) / (kWarps * p.tiles_per_warp));
-    if (units > 0x7fffffff / p.chunks) return PA_ERR_UNSUPPORTED;
-    const dim3 g((unsigned)(units * p.chunks)), b(kWarps * 32);
     const int group = p.num_q_heads / p.num_kv_heads;
-    if (dtype == PA_BF16) {
-        if (group == 16)
-            return head_dim == 128 ? launch_scores_mma<128, 2>(p, g, st) : launch_scores_mma<64, 2>(p, g, st);
-        return head_dim == 128 ? launch_scores_mma<128, 1>(p, g, st) : launch_scores_mma<64, 1>(p, g, st);
-    }
     const bool wide = head_dim == 128;
+    if (dtype == PA_BF16) {
+        if (group == 16) return wide ? launch_scores_mma<128, 2>(p, st) : launch_scores_mma<64, 2>(p, st);
+        return wide ? launch_scores_mma<128, 1>(p, st) : launch_scores_mma<64, 1>(p, st);
+    }
     switch (group) {
-        case 1: return launch_pdl(wide ? block_scores_f32_kernel<128, 1> : block_scores_f32_kernel<64, 1>, g, b, 0, st, p);
-        case 2: return launch_pdl(wide ? block_scores_f32_kernel<128, 2> : block_scores_f32_kernel<64, 2>, g, b, 0, st, p);
-        case 4: return launch_pdl(wide ? block_scores_f32_kernel<128, 4> : block_scores_f32_kernel<64, 4>, g, b, 0, st, p);
-        case 8: return launch_pdl(wide ? block_scores_f32_kernel<128, 8> : block_scores_f32_kernel<64, 8>, g, b, 0, st, p);
+        case 1: return wide ? launch_scores_f32<128, 1>(p, st) : launch_scores_f32<64, 1>(p, st);
+        case 2: return wide ? launch_scores_f32<128, 2>(p, st) : launch_scores_f32<64, 2>(p, st);
+        case 4: return wide ? launch_scores_f32<128, 4>(p, st) : launch_scores_f32<64, 4>(p, st);
+        case 8: return wide ? launch_scores_f32<128, 8>(p, st) : launch_scores_f32<64, 8>(p, st);
     }
     return PA_ERR_UNSUPPORTED;
 }

@@ -567,12 +567,13 @@ int launch_sparse(const SparseParams& p, void (*kernel)(SparseParams, int), std:
     // as soon as the lists fill the SMs: at 2048 lists of 64 blocks of 16 tokens
     // 156 us (6.85 TB/s) against 165 with two CTAs and 190 with four; at 128
     // lists 15.6 against 17.8 and 21.3.  Below that, as many as give each SM
-    // one (16 lists of 512 blocks: 72.8 us with one, 16.9 with eight); and three
-    // an SM, which is what its shared memory holds, where each warp then still
-    // has 16 steps (128 lists of 256 blocks: 49.3 us with one, 47.6 with three).
+    // one (16 lists of 512 blocks: 72.8 us with one, 16.9 with eight); or three
+    // an SM, which is what its shared memory holds, if each warp then still has
+    // 16 steps (128 lists of 256 blocks: 49.3 us with one, 55 with two, which
+    // leave some SMs three CTAs and some one, 47.6 with three).
     const int64_t steps = ((int64_t)p.max_selected * p.block_size + step_tokens - 1) / step_tokens;
-    const int64_t fill = num_sms() / units, hold = 3 * num_sms() / units;
-    int64_t splits = std::max(fill, std::min(hold, steps / (kSparseWarps * 16)));
+    const int64_t fill = num_sms() / units, hold = std::min(3 * num_sms() / units, (int64_t)kMaxSplits);
+    int64_t splits = steps >= hold * kSparseWarps * 16 ? hold : fill;
     splits = std::min(splits, std::min((int64_t)kMaxSplits, (steps + kSparseWarps - 1) / kSparseWarps));
     splits = std::max(splits, (int64_t)1);
     if (units > 0x7fffffff / splits) return PA_ERR_UNSUPPORTED;
