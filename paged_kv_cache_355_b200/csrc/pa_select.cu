@@ -11,7 +11,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <atomic>
@@ -259,18 +258,18 @@ struct ScoreParams {
     int64_t num_rows;
     int num_q_heads, num_kv_heads;
     int64_t num_blocks;
-    // a warp takes heads_per_warp kv heads of tiles_per_warp tiles of 16 blocks of
-    // a row: `parts` of the heads and `chunks` of the tiles are CTAs of their own
-    int heads_per_warp, tiles_per_warp, parts, chunks;
+    // a CTA's warps take head_warps kv heads side by side, each tiles_per_warp
+    // tiles of 16 blocks: `parts` CTAs for a row's heads, `chunks` for its tiles
+    int head_warps, tiles_per_warp, parts, chunks;
     int* err;
 };
 
-// This warp's part of a row: `tiles_per_warp` tiles of 16 blocks, every
-// kWarps-th, so that a short row still occupies all warps, and some kv heads.
+// This warp's part of a row: one kv head of `tiles_per_warp` tiles of 16
+// blocks, `stride` tiles apart.
 struct WarpTiles {
     const int32_t* table;
     int64_t row;
-    int h0, heads, blocks, first, end;
+    int h, blocks, first, end, stride;
     bool named, recorder;  // the row's sequence exists; this thread reports a bad row
 };
 
@@ -278,16 +277,16 @@ struct WarpTiles {
 __device__ __forceinline__ WarpTiles warp_tiles(const ScoreParams& p) {
     WarpTiles w;
     const int64_t unit = blockIdx.x / p.chunks;
-    const int chunk = (int)(blockIdx.x - unit * p.chunks);
+    const int chunk = (int)(blockIdx.x - unit * p.chunks), warp = threadIdx.x >> 5;
     w.row = unit / p.parts;
-    w.h0 = (int)(unit - w.row * p.parts) * p.heads_per_warp;
-    w.heads = min(p.heads_per_warp, p.num_kv_heads - w.h0);
+    w.h = (int)(unit - w.row * p.parts) * p.head_warps + (warp & (p.head_warps - 1));
     const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[w.row] : w.row;
     w.named = seq >= 0 && seq < p.batch;
-    w.recorder = chunk == 0 && w.h0 == 0 && threadIdx.x == 0;
+    w.recorder = chunk == 0 && w.h == 0 && threadIdx.x == 0;
     w.table = p.block_tables + (w.named ? seq : 0) * p.max_blocks_per_seq;
-    w.first = chunk * kWarps * p.tiles_per_warp + (threadIdx.x >> 5);
-    w.end = w.first + kWarps * p.tiles_per_warp;
+    w.stride = kWarps / p.head_warps;
+    w.first = chunk * w.stride * p.tiles_per_warp + warp / p.head_warps;
+    w.end = w.h < p.num_kv_heads ? w.first + w.stride * p.tiles_per_warp : 0;
     w.blocks = 0;
     return w;
 }
@@ -325,19 +324,20 @@ __device__ __forceinline__ int32_t block_of(const ScoreParams& p, const WarpTile
 struct Entries {
     int32_t e0, e1;
     int j, last, pair;
-    static constexpr int kPair = 2 * kWarps * 16;  // blocks between a lane's blocks of two pairs
+    int apart;  // blocks between a lane's blocks of two pairs
 
     // Reads beside the row's length; false where the warp has no tile.
     __device__ __forceinline__ bool open(const ScoreParams& p, WarpTiles& w) {
         const int lane = threadIdx.x & 31;
-        j = (w.first + (lane >> 4) * kWarps) * 16 + (lane & 15);
+        j = (w.first + (lane >> 4) * w.stride) * 16 + (lane & 15);
+        apart = 2 * 16 * w.stride;
         e0 = entry_of(p, w, j);
-        e1 = entry_of(p, w, j + kPair);
+        e1 = entry_of(p, w, j + apart);
         end_tiles(p, w);
         if (w.first >= w.end) return false;
         last = w.end * 16;  // blocks of other CTAs lie behind
         e0 = j < last ? block_of(p, w, j, e0) : -1;
-        j += kPair;
+        j += apart;
         e1 = j < last ? block_of(p, w, j, e1) : -1;
         pair = 0;
         return true;
@@ -348,7 +348,7 @@ struct Entries {
     __device__ __forceinline__ void next_pair(const ScoreParams& p, const WarpTiles& w) {
         ++pair;
         e0 = e1;
-        j += kPair;
+        j += apart;
         e1 = j < last ? block_of(p, w, j, entry_of(p, w, j)) : -1;
     }
 };
@@ -361,116 +361,92 @@ struct Entries {
 // asynchronously into a ring of two tiles that belongs to the warp alone.
 // 16-byte chunk c of block b lies at c ^ (b & 7), so that the eight rows of a
 // matrix load touch all banks.
-// HEADS: the warp goes through several kv heads of each tile and reloads q.
-template <int D, int NT, bool HEADS>
-__global__ void __launch_bounds__(kWarps * 32, 3) block_scores_mma_kernel(const ScoreParams p) {
+template <int D, int NT, int STAGES>
+__global__ void __launch_bounds__(kWarps * 32, STAGES == 1 ? (NT == 1 ? 5 : 4) : 3) block_scores_mma_kernel(const ScoreParams p) {
     constexpr int kRowBytes = 4 * D;            // lo and hi of one block
     constexpr int kTile = 16 * kRowBytes;
     constexpr int kRowLanes = D / 4;            // lanes that copy one block
     constexpr int kCopyRows = 32 / kRowLanes;
     constexpr int kSteps = D / 16;
-    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][2][16 blocks][lo, hi]
+    extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][16 blocks][lo, hi]
     griddep_wait();
     griddep_launch_dependents();
     WarpTiles w = warp_tiles(p);
     Entries e;
     if (!e.open(p, w)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int heads = HEADS ? w.heads : 1;
-    const int tiles = (w.end - w.first + kWarps - 1) / kWarps;
+    const int tiles = (w.end - w.first + w.stride - 1) / w.stride;
 
     const int group = p.num_q_heads / p.num_kv_heads;
     const int copy_row = lane / kRowLanes, copy_chunk = lane % kRowLanes;
-    const __nv_bfloat16* bounds = static_cast<const __nv_bfloat16*>(p.key_bounds) + (int64_t)w.h0 * 2 * D + 8 * copy_chunk;
+    const __nv_bfloat16* bounds = static_cast<const __nv_bfloat16*>(p.key_bounds) + (int64_t)w.h * 2 * D + 8 * copy_chunk;
     const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
-    const uint32_t slots = smem_addr(ring) + warp * (2 * kTile);
+    const uint32_t slots = smem_addr(ring) + warp * (STAGES * kTile);
     const uint32_t copy_dst = slots + copy_row * kRowBytes;
-    int f_tile = 0, f_head = 0;  // the next to be fetched
+    int fetched = 0;
     auto fetch = [&](int stage) {
-        if (f_tile < tiles) {
-            const __nv_bfloat16* src = bounds + f_head * (2 * D);
+        if (fetched < tiles) {
 #pragma unroll
             for (int u = 0; u < 16; u += kCopyRows) {
-                const int32_t blk = e.at(f_tile, u + copy_row);
+                const int32_t blk = e.at(fetched, u + copy_row);
                 const uint32_t dst = copy_dst + stage * kTile + u * kRowBytes + ((copy_chunk ^ ((u + copy_row) & 7)) << 4);
-                copy_async16(dst, src + (blk < 0 ? 0 : blk) * block_stride, blk >= 0);
+                copy_async16(dst, bounds + (blk < 0 ? 0 : blk) * block_stride, blk >= 0);
             }
-            if (++f_head == heads) {
-                f_head = 0;
-                ++f_tile;
-            }
+            ++fetched;
         }
         copy_async_commit();
     };
-    fetch(0);
-    fetch(1);
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) fetch(st);
 
     // column 8 n + g of Q^T; its negative values (side 0) meet lo, the others hi
-    uint32_t q[HEADS ? 1 : 2][NT][kSteps][2];
-    auto part = [](uint32_t x, int side) {
-        uint32_t neg;  // the sign of each half, all over it
-        asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(x));
-        return side ? x & ~neg : x & neg;
-    };
-    auto load_q = [&](int head) {
+    uint32_t q[2][NT][kSteps][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                       (w.row * p.num_q_heads + (w.h0 + head) * group + (8 * n + g) % group) * D + 2 * t;
+    for (int n = 0; n < NT; ++n) {
+        const __nv_bfloat16* src =
+            static_cast<const __nv_bfloat16*>(p.q) + (w.row * p.num_q_heads + w.h * group + (8 * n + g) % group) * D + 2 * t;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c);
-                    if (HEADS) {
-                        q[0][n][i][c] = x;
-                    } else {
-                        q[0][n][i][c] = part(x, 0);
-                        q[HEADS ? 0 : 1][n][i][c] = part(x, 1);
-                    }
-                }
-        }
-    };
-    load_q(0);
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * c);
+                uint32_t neg;  // the sign of each half, all over it
+                asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(x));
+                q[0][n][i][c] = x & neg;
+                q[1][n][i][c] = x & ~neg;
+            }
+    }
     // matrix loads: lane = (matrix, row), the matrices (8 blocks, chunk of 8 channels)
     const uint32_t mat_row = lane & 7, mat_lo = (lane >> 3) & 1, mat_hi = lane >> 4;
     const uint32_t mat = slots + (mat_lo * 8 + mat_row) * kRowBytes + ((mat_hi ^ mat_row) << 4);
+    float* out = p.scores + (w.row * p.num_kv_heads + w.h) * p.score_stride + w.first * 16;
     int stage = 0;
-    for (int tile = 0; tile < tiles; ++tile) {
+    for (int tile = 0; tile < tiles; ++tile, stage ^= STAGES - 1, out += w.stride * 16) {
         const unsigned have = __ballot_sync(0xffffffffu, e.e0 >= 0) >> (16 * (tile & 1));
-        for (int head = 0; head < heads; ++head, stage ^= 1) {
-            copy_async_wait<1>();
-            __syncwarp();  // every lane's copies are in
-            float s[2][NT][4] = {};
+        copy_async_wait<STAGES - 1>();
+        __syncwarp();  // every lane's copies are in
+        float s[2][NT][4] = {};
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
+        for (int side = 0; side < 2; ++side)
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    uint32_t a[4];
-                    ldmatrix_x4((mat ^ (i << 5)) + stage * kTile + side * 2 * D, a[0], a[1], a[2], a[3]);
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t a[4];
+                ldmatrix_x4((mat ^ (i << 5)) + stage * kTile + side * 2 * D, a[0], a[1], a[2], a[3]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (HEADS)
-                            mma_bf16_16816(s[side][n], a, part(q[0][n][i][0], side), part(q[0][n][i][1], side));
-                        else
-                            mma_bf16_16816(s[side][n], a, q[HEADS ? 0 : side][n][i][0], q[HEADS ? 0 : side][n][i][1]);
-                    }
-                }
-            __syncwarp();  // every lane has read the stage
-            fetch(stage);
-            if (HEADS) load_q(head + 1 == heads ? 0 : head + 1);
-            // heads 2 t, 2 t + 1 (+ 8) of blocks g and g + 8
-            float* out = p.scores + (w.row * p.num_kv_heads + w.h0 + head) * p.score_stride + (w.first + tile * kWarps) * 16;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                float best = max_nan(s[0][0][2 * a] + s[1][0][2 * a], s[0][0][2 * a + 1] + s[1][0][2 * a + 1]);
-                if (NT == 2)
-                    best = max_nan(best, max_nan(s[0][NT - 1][2 * a] + s[1][NT - 1][2 * a],
-                                                 s[0][NT - 1][2 * a + 1] + s[1][NT - 1][2 * a + 1]));
-                best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 1));
-                best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 2));
-                if (t == a && (have >> (g + 8 * a) & 1)) out[g + 8 * a] = best;
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[side][n], a, q[side][n][i][0], q[side][n][i][1]);
             }
+        __syncwarp();  // every lane has read the stage
+        fetch(stage);
+        // heads 2 t, 2 t + 1 (+ 8) of blocks g and g + 8
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            float best = max_nan(s[0][0][2 * a] + s[1][0][2 * a], s[0][0][2 * a + 1] + s[1][0][2 * a + 1]);
+            if (NT == 2)
+                best = max_nan(best, max_nan(s[0][NT - 1][2 * a] + s[1][NT - 1][2 * a],
+                                             s[0][NT - 1][2 * a + 1] + s[1][NT - 1][2 * a + 1]));
+            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            if (t == a && (have >> (g + 8 * a) & 1)) out[g + 8 * a] = best;
         }
         if (tile & 1) e.next_pair(p, w);
     }
@@ -497,78 +473,71 @@ __global__ void __launch_bounds__(kWarps * 32, 3) block_scores_f32_kernel(const 
     Entries e;
     if (!e.open(p, w)) return;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, x = lane % kLanes;
-    const int tiles = (w.end - w.first + kWarps - 1) / kWarps;
+    const int tiles = (w.end - w.first + w.stride - 1) / w.stride;
     float4 neg[G], pos[G];  // q's negative values, which meet lo, and the others
-    const float* bounds = static_cast<const float*>(p.key_bounds) + (int64_t)w.h0 * 2 * D + 4 * x;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                                          (w.row * p.num_q_heads + w.h * G + i) * D + 4 * x);
+        neg[i] = make_float4(q.x < 0.f ? q.x : 0.f, q.y < 0.f ? q.y : 0.f, q.z < 0.f ? q.z : 0.f, q.w < 0.f ? q.w : 0.f);
+        pos[i] = make_float4(q.x < 0.f ? 0.f : q.x, q.y < 0.f ? 0.f : q.y, q.z < 0.f ? 0.f : q.z, q.w < 0.f ? 0.f : q.w);
+    }
+    const float* bounds = static_cast<const float*>(p.key_bounds) + (int64_t)w.h * 2 * D + 4 * x;
     const int64_t block_stride = (int64_t)p.num_kv_heads * 2 * D;
     uint8_t* mine = ring + (threadIdx.x >> 5) * (kStages * kPiece) + lane * 16;
-    int f_tile = 0, f_head = 0, f_part = 0;
+    int f_tile = 0, f_part = 0;
     auto fetch = [&](int stage) {
         if (f_tile < tiles) {
             const uint32_t dst = smem_addr(mine) + stage * kPiece;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int32_t blk = e.at(f_tile, (f_part * kBlocks + b) * kRows + sub);
-                const float* src = bounds + f_head * (2 * D) + (blk < 0 ? 0 : blk) * block_stride;
+                const float* src = bounds + (blk < 0 ? 0 : blk) * block_stride;
                 copy_async16(dst + b * 1024, src, blk >= 0);
                 copy_async16(dst + b * 1024 + 512, src + D, blk >= 0);
             }
             if (++f_part == kPerTile) {
                 f_part = 0;
-                if (++f_head == w.heads) {
-                    f_head = 0;
-                    ++f_tile;
-                }
+                ++f_tile;
             }
         }
         copy_async_commit();
     };
 #pragma unroll
     for (int st = 0; st < kStages; ++st) fetch(st);
+    float* out = p.scores + (w.row * p.num_kv_heads + w.h) * p.score_stride + w.first * 16;
     int stage = 0;
-    for (int tile = 0; tile < tiles; ++tile) {
+    for (int tile = 0; tile < tiles; ++tile, out += w.stride * 16) {
         const unsigned have = __ballot_sync(0xffffffffu, e.e0 >= 0) >> (16 * (tile & 1));
-        for (int head = 0; head < w.heads; ++head) {
-            if (tile == 0 || w.heads > 1) {
+        for (int part = 0; part < kPerTile; ++part, stage = (stage + 1) % kStages) {
+            copy_async_wait<kStages - 1>();
+            const float4* rows = reinterpret_cast<const float4*>(mine + stage * kPiece);
+            float v[kBlocks * G];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const float4 lo = rows[b * 64], hi = rows[b * 64 + 32];
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
-                    const float4 q = *reinterpret_cast<const float4*>(
-                        static_cast<const float*>(p.q) + (w.row * p.num_q_heads + (w.h0 + head) * G + i) * D + 4 * x);
-                    neg[i] = make_float4(q.x < 0.f ? q.x : 0.f, q.y < 0.f ? q.y : 0.f, q.z < 0.f ? q.z : 0.f, q.w < 0.f ? q.w : 0.f);
-                    pos[i] = make_float4(q.x < 0.f ? 0.f : q.x, q.y < 0.f ? 0.f : q.y, q.z < 0.f ? 0.f : q.z, q.w < 0.f ? 0.f : q.w);
+                    float a = neg[i].x * lo.x, c = pos[i].x * hi.x;
+                    a = fmaf(neg[i].y, lo.y, a);
+                    c = fmaf(pos[i].y, hi.y, c);
+                    a = fmaf(neg[i].z, lo.z, a);
+                    c = fmaf(pos[i].z, hi.z, c);
+                    a = fmaf(neg[i].w, lo.w, a);
+                    c = fmaf(pos[i].w, hi.w, c);
+                    v[b * G + i] = a + c;
                 }
             }
-            float* out = p.scores + (w.row * p.num_kv_heads + w.h0 + head) * p.score_stride + (w.first + tile * kWarps) * 16;
-            for (int part = 0; part < kPerTile; ++part, stage = (stage + 1) % kStages) {
-                copy_async_wait<kStages - 1>();
-                const float4* rows = reinterpret_cast<const float4*>(mine + stage * kPiece);
-                float v[kBlocks * G];
+            fetch(stage);
+            reduce_scatter<kBlocks * G, kLanes>(v);
+            // lane x holds heads of block x / (kLanes / kBlocks)
+            float best = v[0];
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    const float4 lo = rows[b * 64], hi = rows[b * 64 + 32];
+            for (int i = 1; i < kHeld; ++i) best = max_nan(best, v[i]);
 #pragma unroll
-                    for (int i = 0; i < G; ++i) {
-                        float a = neg[i].x * lo.x, c = pos[i].x * hi.x;
-                        a = fmaf(neg[i].y, lo.y, a);
-                        c = fmaf(pos[i].y, hi.y, c);
-                        a = fmaf(neg[i].z, lo.z, a);
-                        c = fmaf(pos[i].z, hi.z, c);
-                        a = fmaf(neg[i].w, lo.w, a);
-                        c = fmaf(pos[i].w, hi.w, c);
-                        v[b * G + i] = a + c;
-                    }
-                }
-                fetch(stage);
-                reduce_scatter<kBlocks * G, kLanes>(v);
-                // lane x holds heads of block x / (kLanes / kBlocks)
-                float best = v[0];
-#pragma unroll
-                for (int i = 1; i < kHeld; ++i) best = max_nan(best, v[i]);
-#pragma unroll
-                for (int m = kLanes / kBlocks / 2; m; m >>= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, m));
-                const int block = (part * kBlocks + x / (kLanes / kBlocks)) * kRows + sub;
-                if (x % (kLanes / kBlocks) == 0 && (have >> block & 1)) out[block] = best;
-            }
+            for (int m = kLanes / kBlocks / 2; m; m >>= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, m));
+            const int block = (part * kBlocks + x / (kLanes / kBlocks)) * kRows + sub;
+            if (x % (kLanes / kBlocks) == 0 && (have >> block & 1)) out[block] = best;
         }
         if (tile & 1) e.next_pair(p, w);
     }
@@ -855,11 +824,11 @@ int launch_scores_kernel(const ScoreParams& p, void (*kernel)(ScoreParams), std:
 }
 
 template <int D, int NT>
-int launch_scores_mma(const ScoreParams& p, cudaStream_t st) {
-    constexpr int kSmem = kWarps * 2 * 16 * 4 * D;
-    static std::atomic<unsigned long long> one{0}, several{0};
-    return p.heads_per_warp > 1 ? launch_scores_kernel(p, block_scores_mma_kernel<D, NT, true>, several, kSmem, st)
-                                : launch_scores_kernel(p, block_scores_mma_kernel<D, NT, false>, one, kSmem, st);
+int launch_scores_mma(const ScoreParams& p, bool brief, cudaStream_t st) {
+    constexpr int kTile = kWarps * 16 * 4 * D;
+    static std::atomic<unsigned long long> one{0}, two{0};
+    return brief ? launch_scores_kernel(p, block_scores_mma_kernel<D, NT, 1>, one, kTile, st)
+                 : launch_scores_kernel(p, block_scores_mma_kernel<D, NT, 2>, two, 2 * kTile, st);
 }
 
 template <int D, int G>
@@ -871,21 +840,27 @@ int launch_scores_f32(const ScoreParams& p, cudaStream_t st) {
 int launch_scores(ScoreParams p, int head_dim, int dtype, cudaStream_t st) {
     const int64_t tiles = ((int64_t)p.max_context_len + 16 * p.block_size - 1) / (16 * p.block_size);
     const int64_t all = p.num_rows * p.num_kv_heads * tiles, sms = num_sms();
-    // Rows of at most four tiles a warp: most of a ragged batch has far fewer,
-    // so what a warp gets more of is heads, of one tile, whose look-ups they
-    // share.  Longer rows: tiles of one head, up to 8 once the grid has 32 warps
-    // an SM.
-    const char* f = getenv("PA_NH");
-    const int64_t heads = tiles > 4 * kWarps ? 1 : std::max((int64_t)1, std::min((int64_t)p.num_kv_heads, f ? atoi(f) : all / (sms * 24)));
-    p.parts = (int)((p.num_kv_heads + heads - 1) / heads);
-    p.heads_per_warp = (p.num_kv_heads + p.parts - 1) / p.parts;
-    p.tiles_per_warp = p.heads_per_warp > 1 ? 1 : (int)std::max((int64_t)1, std::min((int64_t)8, all / (sms * 32)));
-    p.chunks = (int)((tiles + kWarps * p.tiles_per_warp - 1) / (kWarps * p.tiles_per_warp));
+    // A CTA's warps take heads side by side: they share a row's look-ups, and a
+    // row of one tile has work for all of them (256 rows of one tile, 8 kv
+    // heads: 4.4 us, against 7.1 with a head's tiles side by side).  Four tiles
+    // a warp once the grid has 32 warps an SM (16 contexts of 32k to 131k
+    // tokens: 77 us with one, 49 with four or eight; 256 of up to 4096: 18.5
+    // with one, 13.4 with four, 15.7 with eight).
+    p.head_warps = p.num_kv_heads > 2 ? kWarps : p.num_kv_heads;
+    const int per_cta = kWarps / p.head_warps;  // tiles side by side
+    p.parts = (p.num_kv_heads + p.head_warps - 1) / p.head_warps;
+    p.tiles_per_warp = (int)std::max((int64_t)1, std::min((int64_t)4, all / (sms * 32)));
+    p.chunks = (int)((tiles + per_cta * p.tiles_per_warp - 1) / (per_cta * p.tiles_per_warp));
+    // A ring of two tiles pays where most warps have several: rows of at most 16
+    // tiles are, in a ragged batch, mostly shorter, and better served by five
+    // CTAs an SM with one tile each than by three with two (256 rows of 700
+    // tokens: 10.8 against 12.5 us).
+    const bool brief = tiles <= 16 || p.tiles_per_warp == 1;
     const int group = p.num_q_heads / p.num_kv_heads;
     const bool wide = head_dim == 128;
     if (dtype == PA_BF16) {
-        if (group == 16) return wide ? launch_scores_mma<128, 2>(p, st) : launch_scores_mma<64, 2>(p, st);
-        return wide ? launch_scores_mma<128, 1>(p, st) : launch_scores_mma<64, 1>(p, st);
+        if (group == 16) return wide ? launch_scores_mma<128, 2>(p, brief, st) : launch_scores_mma<64, 2>(p, brief, st);
+        return wide ? launch_scores_mma<128, 1>(p, brief, st) : launch_scores_mma<64, 1>(p, brief, st);
     }
     switch (group) {
         case 1: return wide ? launch_scores_f32<128, 1>(p, st) : launch_scores_f32<64, 1>(p, st);
