@@ -42,7 +42,14 @@ __device__ __forceinline__ void store_out(const SparseParams& p, int64_t at, flo
         static_cast<float*>(p.out)[at] = x;
 }
 
-constexpr int kSparseWarps = 4;
+// Warps of a CTA, each with a ring of 16 KB.  bf16: six, two CTAs an SM, while
+// all lists' CTAs fit the GPU at once, else four, three CTAs an SM, which end
+// more evenly (256 lists of 128 blocks of 16 tokens: 46 us with six, 51 with
+// four; 320 of 64: 37.8 and 33.4; 2048 of 16: 55 and 47.6).  fp32: twelve, one
+// CTA an SM, since a warp computes longer on what it has (128 lists of 128: 50
+// us; with four warps and each list split in three, 53).
+constexpr int kF32Warps = 12;
+constexpr int kRingBytes = 16384;
 constexpr int kMaxSplits = 8;  // the portable cluster size
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -114,11 +121,11 @@ struct Row {
 // Joins the states (running maximum, sum and output of each head) that the
 // CTA's threads left in shared memory, then those of the cluster's CTAs, each
 // CTA finishing its share of the outputs.
-template <int STATES, int HEADS, int D>
+template <int STATES, int HEADS, int D, int WARPS>
 __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r, int splits, float (*s_o)[HEADS][D],
                                             float (*s_m)[HEADS], float (*s_l)[HEADS], float* c_m, float* c_l) {
     const float kNegInf = __int_as_float(0xff800000);
-    constexpr int kThreads = kSparseWarps * 32;
+    constexpr int kThreads = WARPS * 32;
     const int64_t out0 = (r.row * p.num_q_heads + r.h * r.group) * D;
     __syncthreads();
     for (int i = threadIdx.x; i < r.group * D; i += kThreads) {
@@ -187,13 +194,13 @@ __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r,
 // P is split into a bf16 value and a bf16 remainder (two products), so that
 // its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
 // once (2^-9) would be half of a bf16 output's own error.
-// One cluster of `splits` CTAs per (row, kv head): its splits * 4 warps take
+// One cluster of `splits` CTAs per (row, kv head): its splits * WARPS warps take
 // the tiles of the list in turn, each with its own running maximum and sum, and
 // the states are joined through the cluster's shared memory, so that a long
 // list of few rows fills the GPU without a workspace or a second launch.
 // NT: 8-wide tiles of query heads (2 for a group of 16).
-template <int D, int NT, int kStages>
-__global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const SparseParams p, int splits) {
+template <int D, int NT, int kStages, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) sparse_mma_kernel(const SparseParams p, int splits) {
     constexpr int kHeads = 8 * NT;             // query heads, the group padded with zero rows
     constexpr int kRowBytes = 2 * D;
     constexpr int kTile = 16 * kRowBytes;      // K or V of one tile of 16 tokens
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const 
     constexpr int kRowLanes = D / 8;           // lanes that copy one row
     constexpr int kCopyRows = 32 / kRowLanes;  // rows of one copy instruction
     extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][K, V][16 tokens][D], later the states
-    __shared__ float s_m[kSparseWarps][kHeads], s_l[kSparseWarps][kHeads], c_m[kHeads], c_l[kHeads];
+    __shared__ float s_m[WARPS][kHeads], s_l[WARPS][kHeads], c_m[kHeads], c_l[kHeads];
     const float kNegInf = __int_as_float(0xff800000);
     griddep_wait();
     griddep_launch_dependents();
@@ -215,11 +222,11 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const 
     const int per_block = p.block_size / 8;  // half-tiles
     const int shift = per_block == 1 ? 0 : per_block == 2 ? 1 : 2;
     const int64_t halves = (int64_t)p.max_selected * per_block;
-    const int step = splits * kSparseWarps;  // warps of the cluster
+    const int step = splits * WARPS;  // warps of the cluster
     const int64_t tiles = (halves + 1) / 2;
     Row r;
     r.rank = splits > 1 ? cluster_rank() : 0;
-    int64_t first = (int64_t)r.rank * kSparseWarps + warp;
+    int64_t first = (int64_t)r.rank * WARPS + warp;
     int64_t half = (first + (int64_t)(lane >> 1) * step) * 2 + (lane & 1);
     int entry = r.open(p, splits, half, halves, shift);
 
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const 
                 s_o[warp][head][16 * i + g + 8] = o[n][i][c + 2];
             }
         }
-    join_states<kSparseWarps, kHeads, D>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
+    join_states<WARPS, kHeads, D, WARPS>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
 }
 
 // ---------------------------------------------------------------------------
@@ -391,17 +398,17 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_mma_kernel(const 
 // weight is computed by one lane or few, and reaches the others through shared
 // memory.
 template <int D, int G, int kStages>
-__global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_f32_kernel(const SparseParams p, int splits) {
+__global__ void __launch_bounds__(kF32Warps * 32, 1) sparse_f32_kernel(const SparseParams p, int splits) {
     constexpr int kLanes = D / 4;
     constexpr int kRows = 32 / kLanes;        // tokens side by side
     constexpr int kOwn = 8 / kRows;           // tokens of a lane group in a half-tile
     constexpr int kStage = 2 * 8 * D * 4;     // K and V of a half-tile
-    constexpr int kStates = kSparseWarps * kRows;
+    constexpr int kStates = kF32Warps * kRows;
     constexpr int kValues = 4 * G;            // scores of 4 tokens
     constexpr int kHeld = kValues > kLanes ? kValues / kLanes : 1;  // of them in a lane
     extern __shared__ __align__(1024) uint8_t ring[];  // [warp][stage][K, V][row][lane], later the states
     __shared__ float s_m[kStates][G], s_l[kStates][G], c_m[G], c_l[G];
-    __shared__ __align__(16) float s_p[kSparseWarps][kRows][kValues];
+    __shared__ __align__(16) float s_p[kF32Warps][kRows][kValues];
     const float kNegInf = __int_as_float(0xff800000);
     griddep_wait();
     griddep_launch_dependents();
@@ -411,10 +418,10 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_f32_kernel(const 
     const int per_block = p.block_size / 8;
     const int shift = per_block == 1 ? 0 : per_block == 2 ? 1 : 2;
     const int64_t halves = (int64_t)p.max_selected * per_block;
-    const int step = splits * kSparseWarps;
+    const int step = splits * kF32Warps;
     Row r;
     r.rank = splits > 1 ? cluster_rank() : 0;
-    int64_t first = (int64_t)r.rank * kSparseWarps + warp;  // this warp's half-tiles, 32 at a time
+    int64_t first = (int64_t)r.rank * kF32Warps + warp;  // this warp's half-tiles, 32 at a time
     int64_t half = first + (int64_t)lane * step;
     int entry = r.open(p, splits, half, halves, shift);
 
@@ -546,40 +553,36 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 3) sparse_f32_kernel(const 
     }
 #pragma unroll
     for (int i = 0; i < G; ++i) *reinterpret_cast<float4*>(&s_o[state][i][4 * x]) = o[i];
-    join_states<kStates, G, D>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
+    join_states<kStates, G, D, kF32Warps>(p, r, splits, s_o, s_m, s_l, c_m, c_l);
 }
 
 // `step_tokens`: tokens that a warp takes at a time.
 int launch_sparse(const SparseParams& p, void (*kernel)(SparseParams, int), std::atomic<unsigned long long>& configured,
-                  size_t smem, int step_tokens, cudaStream_t st) {
+                  int warps, int step_tokens, cudaStream_t st) {
+    const int smem = warps * kRingBytes;
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return PA_ERR_CUDA;
         configured.fetch_or(bit);
     }
     const int64_t units = p.num_rows * p.num_kv_heads;
     // half-tiles are counted in 32 bits (a pool that needs more is 4 TB)
     if (p.num_blocks > (1ll << 32) / (p.num_kv_heads * (p.block_size / 8))) return PA_ERR_UNSUPPORTED;
-    // One CTA a list keeps its four warps longest in their stream, and is best
-    // as soon as the lists fill the SMs: at 2048 lists of 64 blocks of 16 tokens
-    // 156 us (6.85 TB/s) against 165 with two CTAs and 190 with four; at 128
-    // lists 15.6 against 17.8 and 21.3.  Below that, as many as give each SM
-    // one (16 lists of 512 blocks: 72.8 us with one, 16.9 with eight); or three
-    // an SM, which is what its shared memory holds, if each warp then still has
-    // 16 steps (128 lists of 256 blocks: 49.3 us with one, 55 with two, which
-    // leave some SMs three CTAs and some one, 47.6 with three).
+    // One CTA a list keeps its warps longest in their stream: at 128 lists of 256
+    // blocks of 16 tokens 45.3 us, against 48.2 with two and 52.8 with three.
+    // Fewer lists are split over as many CTAs as leave each SM one (64 lists of
+    // 128 blocks: 19.5 us with one, 17.8 with two; 8 lists: 15.1 with one, 6.7
+    // with eight).
     const int64_t steps = ((int64_t)p.max_selected * p.block_size + step_tokens - 1) / step_tokens;
-    const int64_t fill = num_sms() / units, hold = std::min(3 * num_sms() / units, (int64_t)kMaxSplits);
-    int64_t splits = steps >= hold * kSparseWarps * 16 ? hold : fill;
-    splits = std::min(splits, std::min((int64_t)kMaxSplits, (steps + kSparseWarps - 1) / kSparseWarps));
+    int64_t splits = std::min(num_sms() / units, std::min((int64_t)kMaxSplits, (steps + warps - 1) / warps));
     splits = std::max(splits, (int64_t)1);
     if (units > 0x7fffffff / splits) return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * splits));
-    cfg.blockDim = dim3(kSparseWarps * 32);
+    cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -598,23 +601,26 @@ int launch_sparse(const SparseParams& p, void (*kernel)(SparseParams, int), std:
     return launch_status();
 }
 
-// Rings of 16 KB a warp, 64 KB a CTA, three CTAs an SM.
-constexpr size_t kRing = (size_t)kSparseWarps * 16384;
+template <int D, int NT, int WARPS>
+int launch_mma_warps(const SparseParams& p, cudaStream_t st) {
+    constexpr int kStages = kRingBytes / (2 * 16 * 2 * D);
+    static_assert(NT * 8 * D * 4 <= kRingBytes, "the states fit in the ring");
+    static std::atomic<unsigned long long> configured{0};
+    return launch_sparse(p, sparse_mma_kernel<D, NT, kStages, WARPS>, configured, WARPS, 16, st);
+}
 
 template <int D, int NT>
 int launch_mma(const SparseParams& p, cudaStream_t st) {
-    constexpr int kStages = 16384 / (2 * 16 * 2 * D);
-    static_assert((size_t)kSparseWarps * NT * 8 * D * 4 <= kRing, "the states fit in the ring");
-    static std::atomic<unsigned long long> configured{0};
-    return launch_sparse(p, sparse_mma_kernel<D, NT, kStages>, configured, kRing, 16, st);
+    return p.num_rows * p.num_kv_heads <= 2 * num_sms() ? launch_mma_warps<D, NT, 6>(p, st)
+                                                        : launch_mma_warps<D, NT, 4>(p, st);
 }
 
 template <int D, int G>
 int launch_f32(const SparseParams& p, cudaStream_t st) {
-    constexpr int kStages = 16384 / (2 * 8 * 4 * D);
-    static_assert((size_t)kSparseWarps * (128 / D) * G * D * 4 <= kRing, "the states fit in the ring");
+    constexpr int kStages = kRingBytes / (2 * 8 * 4 * D);
+    static_assert((128 / D) * G * D * 4 <= kRingBytes, "the states fit in the ring");
     static std::atomic<unsigned long long> configured{0};
-    return launch_sparse(p, sparse_f32_kernel<D, G, kStages>, configured, kRing, 8, st);
+    return launch_sparse(p, sparse_f32_kernel<D, G, kStages>, configured, kF32Warps, 8, st);
 }
 
 template <int D>
