@@ -72,11 +72,12 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     const int slice = (int)(blockIdx.x - token * p.slices);
     const int lane = threadIdx.x;
     const int sub = lane / kLanes, x = lane % kLanes;
-    // the lane's elements: 4 from `own` and 4 from own + other; past the rotated
-    // part, or where neighbours pair, they follow one another
+    // the lane's elements: 4 from `own` and 4 from own + other, of the two halves
+    // of the rotated part or of what is past it, so that the lanes' accesses lie
+    // side by side; 8 together where neighbours pair
     const bool turned = WHOLE || x * kChunk < p.rotary_dim;
-    const int own = NEIGHBOURS || !turned ? x * 8 : x * 4;
-    const int other = NEIGHBOURS || !turned ? 4 : WHOLE ? D / 2 : p.rotary_dim / 2;
+    const int own = NEIGHBOURS ? x * 8 : turned ? x * 4 : p.rotary_dim / 2 + x * 4;
+    const int other = NEIGHBOURS ? 4 : WHOLE ? D / 2 : turned ? p.rotary_dim / 2 : (D - p.rotary_dim) / 2;
 
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
     const int q_steps = (Hq + kHeads - 1) / kHeads, kv_steps = (Hkv + kHeads - 1) / kHeads;
