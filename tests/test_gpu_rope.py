@@ -214,6 +214,32 @@ def test_layouts(pa):
     assert pa.pa_read_error_flag() == 0
 
 
+def test_token_strides_of_whole_vectors_only(pa):
+    c = Case(3, 2, 1, 64, 16, "bf16", 64, seed=4)
+    odd = torch.zeros(3, 4 * 64 + 4, dtype=torch.bfloat16, device="cuda")[:, : 4 * 64].view(3, 4, 64)
+    out, kp, vp = c.query_out.cuda(), c.k_pool.cuda(), c.v_pool.cuda()
+    with pytest.raises(pa.PAError, match="PA_ERR_INVALID_ARG"):  # 520 bytes between tokens
+        pa.pa_rope_and_cache(*c.split(odd), out, kp, vp, c.slots.cuda(), c.positions.cuda(), c.cos_sin.cuda())
+    with pytest.raises(TypeError, match="k_pool must be torch.bfloat16"):
+        pa.pa_rope_and_cache(*c.split(c.qkv.cuda()), out, kp.float(), vp, c.slots.cuda(), c.positions.cuda(),
+                             c.cos_sin.cuda())
+    with pytest.raises(TypeError, match="cos_sin must be torch.float32"):
+        pa.pa_rope_and_cache(*c.split(c.qkv.cuda()), out, kp, vp, c.slots.cuda(), c.positions.cuda(),
+                             c.cos_sin.cuda().double())
+    with pytest.raises(TypeError, match="slot_mapping must be a CUDA tensor"):
+        pa.pa_rope_and_cache(*c.split(c.qkv.cuda()), out, kp, vp, c.slots, c.positions.cuda(), c.cos_sin.cuda())
+    assert torch.equal(kp.cpu(), c.k_pool)
+    # one token may lie anywhere, and positions may be one row
+    one = Case(1, 2, 1, 64, 16, "bf16", 64, seed=8)
+    row = torch.zeros(1, 4 * 64 + 4, dtype=torch.bfloat16, device="cuda")[:, : 4 * 64].view(1, 4, 64)
+    row.copy_(one.qkv)
+    out, kp, vp = one.query_out.cuda(), one.k_pool.cuda(), one.v_pool.cuda()
+    pa.pa_rope_and_cache(*one.split(row), out, kp, vp, one.slots.cuda(), one.positions[0].cuda(), one.cos_sin.cuda(),
+                         q_weight=one.q_weight.cuda(), k_weight=one.k_weight.cuda())
+    one.check(out, kp, vp)
+    assert pa.pa_read_error_flag() == 0
+
+
 def test_no_tokens_and_far_positions(pa):
     c = Case(0, 4, 2, 64, 16, "f32", 64)
     before = c.k_pool.clone()
@@ -259,6 +285,24 @@ def test_bad_sequences_of_the_decode_form(pa):
     assert got.tolist() == slots.tolist()
     c.check(out, kp, vp, slots=slots, positions=(lens - 1)[None].clamp(min=0))
     assert pa.pa_read_error_flag() == 5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinite_elements_stay_in_their_pair(pa, dtype):
+    """An infinity past the rotated part, or in one pair, leaves the rest alone."""
+    c = Case(2, 2, 1, 64, 16, dtype, 32, (False, False), seed=5)
+    for interleaved in (False, True):
+        clean = call(pa, c, interleaved)[0]
+        c.qkv[0, 0, 40] = float("inf")
+        c.qkv[1, 1, 3] = float("inf")
+        out = call(pa, c, interleaved)[0]
+        assert out[0, 0, 40] == float("inf")
+        out[0, 0, 40] = clean[0, 0, 40]
+        touched = [2, 3] if interleaved else [3, 19]
+        assert not out[1, 1, touched].isfinite().any()
+        out[1, 1, touched] = clean[1, 1, touched]
+        assert torch.equal(out, clean)
+        c = Case(2, 2, 1, 64, 16, dtype, 32, (False, False), seed=5)
 
 
 def test_nan_rows_stay_in_their_head(pa):

@@ -79,6 +79,19 @@ def test_bounds(pa, dtype, d, bs):
     assert pa.pa_read_error_flag() == 0
 
 
+def test_bounds_of_shared_blocks(pa):
+    """Sequences that share a prompt's full blocks: every one may bring them up to date."""
+    k = torch.randn(7, 2, 8, 64).bfloat16()
+    tables, lens = [[4, 1, 2], [4, 1, 5], [4, 1, 6]], [19, 24, 17]
+    want = np.zeros((7, 2, 2, 64))
+    rs.update_key_bounds(f64(k), want, tables, lens, lens)
+    got = torch.zeros(7, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pa.pa_update_key_bounds(k.cuda(), got, i32(tables).cuda(), i32(lens).cuda(),
+                            query_start=i32([0, 19, 43, 60]).cuda(), max_query_len=24)
+    assert np.array_equal(f64(got), want)
+    assert pa.pa_read_error_flag() == 0
+
+
 def test_bounds_special_values(pa):
     """NaN keys give NaN; infinities and zeros of both signs keep their order."""
     k = torch.zeros(2, 1, 8, 64, dtype=torch.bfloat16)
@@ -155,6 +168,24 @@ def test_scores(pa, dtype, d, group):
 def test_scores_of_several_rows_a_sequence(pa):
     case, kb = score_inputs([40, 300], 8, 2, 128, 16, "bf16")
     check_scores(pa, case, kb, 16, seqs=[1, 1, 0, 1, 0], lens=[298, 299, 40, 300, 1])
+    assert pa.pa_read_error_flag() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hkv,rows", [(1, 3), (2, 2), (5, 200), (8, 40)])
+def test_scores_of_batches_and_head_counts(pa, dtype, hkv, rows):
+    """Head counts that leave warps of a CTA without a head, and batches on both
+    sides of each choice of tiles a warp."""
+    g = torch.Generator().manual_seed(rows)
+    lens = torch.randint(0, 700, (rows,), generator=g).tolist()
+    case, kb = score_inputs(lens, 2 * hkv, hkv, 64, 8, dtype, seed=hkv)
+    check_scores(pa, case, kb, 8)
+    assert pa.pa_read_error_flag() == 0
+
+
+def test_scores_of_a_long_row_among_short_ones(pa):
+    case, kb = score_inputs([30000, 1, 700, 0, 12345], 4, 2, 64, 8, "bf16", seed=6)
+    check_scores(pa, case, kb, 8)
     assert pa.pa_read_error_flag() == 0
 
 
