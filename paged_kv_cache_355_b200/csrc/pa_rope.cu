@@ -53,10 +53,15 @@ struct RopeParams {
     int64_t num_tokens;
     int num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
-    int steps;   // of one warp; a step is 32 / (D / 8) head rows of q, k or v
-    int slices;  // warps of one token
+    int batch;    // steps loaded together, of q, of k or of v; a step is 32 / (D / 8) head rows
+    int batches;  // of one warp
+    int slices;   // warps of one token
     int* err;
 };
+
+// Steps loaded together: 16 registers.
+template <typename T>
+constexpr int kMostSteps = sizeof(T) == 2 ? 4 : 2;
 
 // One warp is one CTA, so that all that depends on its token and step alone is
 // the same for the whole CTA and stays off the lanes.
@@ -64,7 +69,7 @@ template <typename T, int D, bool NEIGHBOURS, bool WHOLE, bool DECODE>  // WHOLE
 __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) {
     constexpr int kLanes = D / kChunk;              // lanes of one head row
     constexpr int kHeads = 32 / kLanes;             // head rows of a step
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // steps loaded together, 16 registers
+    constexpr int kAhead = kMostSteps<T>;
     __shared__ __align__(16) float cs[2][D / 2];    // the token's cosines and sines
     griddep_wait();
     griddep_launch_dependents();
@@ -80,22 +85,24 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     const int other = NEIGHBOURS ? 4 : WHOLE ? D / 2 : turned ? p.rotary_dim / 2 : (D - p.rotary_dim) / 2;
 
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
-    const int q_steps = (Hq + kHeads - 1) / kHeads, kv_steps = (Hkv + kHeads - 1) / kHeads;
-    const int v_first = q_steps + kv_steps;
-    const int first = slice * p.steps, end = min(first + p.steps, v_first + kv_steps);
+    const int batch_heads = p.batch * kHeads;
+    const int q_batches = (Hq + batch_heads - 1) / batch_heads, kv_batches = (Hkv + batch_heads - 1) / batch_heads;
+    const int v_first = q_batches + kv_batches;
+    const int first = slice * p.batches, end = min(first + p.batches, v_first + kv_batches);
     const T* q_src = static_cast<const T*>(p.query) + token * p.q_stride;
     const T* k_src = static_cast<const T*>(p.key) + token * p.k_stride;
     const T* v_src = static_cast<const T*>(p.value) + token * p.v_stride;
     const int src_lane = sub * D + own;
     Chunk<T> rows[kAhead];
-    auto load = [&](Chunk<T>(&to)[kAhead], int from) {
+    auto load = [&](Chunk<T>(&to)[kAhead], int b) {
+        const bool is_q = b < q_batches, is_v = b >= v_first;
+        const int head = (is_q ? b : is_v ? b - v_first : b - q_batches) * batch_heads;
+        const int limit = min(is_q ? Hq : Hkv, head + batch_heads) - sub;
+        const T* src = (is_q ? q_src : is_v ? v_src : k_src) + (int64_t)head * D + src_lane;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int st = from + u;
-            const int head = (st < q_steps ? st : st < v_first ? st - q_steps : st - v_first) * kHeads;
-            const T* src = (st < q_steps ? q_src : st < v_first ? k_src : v_src) + (int64_t)head * D;
             to[u] = Chunk<T>{};
-            if (st < end && head + sub < (st < q_steps ? Hq : Hkv)) to[u].load(src + src_lane, src + src_lane + other);
+            if (head + u * kHeads < limit) to[u].load(src + u * kHeads * D, src + u * kHeads * D + other);
         }
     };
     load(rows, first);  // beside the look-up of where they go
@@ -178,20 +185,23 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     const int64_t head_stride = (int64_t)p.block_size * D;  // between kv heads in the pool
     const int64_t pool_lane = sub * head_stride + own;
 
-    for (int from = first; from < end; from += kAhead) {
+    for (int b = first; b < end; ++b) {
         Chunk<T> next[kAhead];
-        if (from + kAhead < end) load(next, from + kAhead);
+        if (b + 1 < end) load(next, b + 1);
+        const bool is_q = b < q_batches, is_v = b >= v_first;
+        const int head = (is_q ? b : is_v ? b - v_first : b - q_batches) * batch_heads;
+        const int limit = min(is_q ? Hq : Hkv, head + batch_heads);
+        const void* weight = is_q ? p.q_weight : p.k_weight;
+        if (b == first || b == q_batches) coefficients(weight);
+        T* dst = is_q ? q_dst + (int64_t)head * D + src_lane : (is_v ? v_dst : k_dst) + head * head_stride + pool_lane;
+        const int64_t dst_step = is_q ? kHeads * D : kHeads * head_stride;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int st = from + u;
-            if (st >= end) break;
-            const bool is_q = st < q_steps, is_v = st >= v_first;
-            const int head = (is_q ? st : is_v ? st - v_first : st - q_steps) * kHeads;
+            if (head + u * kHeads >= limit) break;  // the same for every lane
             if (!is_v) {
-                if (st == first || st == q_steps) coefficients(is_q ? p.q_weight : p.k_weight);
                 float y[kChunk];
                 rows[u].to_f32(y);
-                if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+                if (weight) {
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) sum = fmaf(y[i], y[i], sum);
@@ -215,9 +225,8 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
                 }
                 rows[u].from_f32(y);
             }
-            T* dst = is_q ? q_dst + (int64_t)head * D + src_lane
-                          : (is_v ? v_dst : k_dst) + head * head_stride + pool_lane;
-            if (head + sub < (is_q ? Hq : Hkv)) rows[u].store(dst, dst + other);
+            if (head + u * kHeads + sub < limit) rows[u].store(dst, dst + other);
+            dst += dst_step;
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) rows[u] = next[u];
@@ -239,8 +248,12 @@ int launch_rope(RopeParams p, bool interleaved, cudaStream_t stream) {
     if (per_warp < 4 && all >= sms * 32) per_warp = 4;
     if (per_warp < 16 && p.num_tokens * ((steps + 15) / 16) >= sms * 28) per_warp = 16;
     per_warp = std::max((int64_t)1, std::min(per_warp, steps));
-    p.slices = (int)((steps + per_warp - 1) / per_warp);
-    p.steps = (int)((steps + p.slices - 1) / p.slices);  // evened out
+    p.batch = (int)std::min(per_warp, (int64_t)kMostSteps<T>);
+    const int batch_heads = p.batch * kHeads;
+    const int64_t batches = (p.num_q_heads + batch_heads - 1) / batch_heads + 2 * ((p.num_kv_heads + batch_heads - 1) / batch_heads);
+    p.slices = (int)((batches * p.batch + per_warp - 1) / per_warp);
+    p.batches = (int)((batches + p.slices - 1) / p.slices);  // evened out
+    p.slices = (int)((batches + p.batches - 1) / p.batches);
     const int64_t blocks = p.num_tokens * p.slices;
     if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     const bool whole = p.rotary_dim == D;
