@@ -126,6 +126,9 @@ struct Range<float> {
 // a lane reads back only what it copied itself, so no barrier is needed.  The
 // whole block is read again for every new token rather than its bounds updated,
 // so that the call can be repeated and follows a copied or rewritten block.
+// Measured: eight prompts, 328k tokens, 8 kv heads of 128, bf16 (688 MB): 104
+// us, 6.6 TB/s, the rate of a copy; fp32 6.7 TB/s; the last blocks of 64
+// sequences (5.6 MB): 3.7 us.
 constexpr int kPieces = 4;
 constexpr int kPieceBytes = 4096;
 
@@ -361,6 +364,9 @@ struct Entries {
 // asynchronously into a ring of two tiles that belongs to the warp alone.
 // 16-byte chunk c of block b lies at c ^ (b & 7), so that the eight rows of a
 // matrix load touch all banks.
+// Measured: 16 contexts of 32k to 131k tokens, 64 / 8 heads of 128 (313 MB): 49
+// us, 6.4 TB/s, 0.97 of a copy; 256 of up to 4096 tokens, 32 / 8 heads (50 MB):
+// 13.3 us.
 template <int D, int NT, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32, STAGES == 1 ? (NT == 1 ? 5 : 4) : 3) block_scores_mma_kernel(const ScoreParams p) {
     constexpr int kRowBytes = 4 * D;            // lo and hi of one block
@@ -456,7 +462,8 @@ __global__ void __launch_bounds__(kWarps * 32, STAGES == 1 ? (NT == 1 ? 5 : 4) :
 // fp32, on the CUDA cores: D / 4 lanes hold the two rows of a block, four
 // channels each, four blocks of a lane group at a time, through a ring of four
 // such pieces (a lane reads back only what it copied); their sums over the
-// lanes by one reduce-scatter.
+// lanes by one reduce-scatter.  Measured: one query head a kv head 6.3 TB/s,
+// eight 5.2 TB/s, bound there by the 16 multiply-adds an 8-byte pair of bounds.
 template <int D, int G>
 __global__ void __launch_bounds__(kWarps * 32, 3) block_scores_f32_kernel(const ScoreParams p) {
     constexpr int kLanes = D / 4;
@@ -610,7 +617,8 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int64_t unit, 
 // Short rows, at most 32 * kItems blocks: one warp a row, its keys in
 // registers.  The value of the last key to be taken is found by bisection, a
 // count over the warp a step, which ends early at any value that exactly
-// max_selected keys reach.
+// max_selected keys reach.  Bound by latency: 2048 rows of up to 256 blocks, 64
+// kept, 6.3 us.
 constexpr int kShortItems = 8;
 
 __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectParams p) {
@@ -674,7 +682,8 @@ __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectP
 // of their own range tell them apart where the leading bits of a radix select
 // would all be the same (and the counters' atomics would collide).  Counts are
 // integers: the order of the atomics changes nothing.  Rows of up to THREADS *
-// kItems blocks are read once, longer ones once a pass.
+// kItems blocks are read once, longer ones once a pass.  Bound by latency and
+// barriers: 128 rows of 2048 to 8192 blocks, 256 kept, 8.6 us.
 constexpr int kBins = 2048;
 constexpr int kItems = 8;
 
@@ -922,7 +931,7 @@ extern "C" int pa_block_scores(const void* q, const void* key_bounds, const int3
         num_q_heads % num_kv_heads != 0)
         return PA_ERR_INVALID_ARG;
     if (!supported_head_dim(head_dim) || !supported_block_size(block_size) ||
-        !supported_group(num_q_heads / num_kv_heads, dtype))
+        !supported_group(num_q_heads / num_kv_heads, dtype) || num_rows > 0x7fffffff)
         return PA_ERR_UNSUPPORTED;
     const int64_t max_blocks = ((int64_t)max_context_len + block_size - 1) / block_size;
     if (max_context_len > (int64_t)max_blocks_per_seq * block_size || score_stride < max_blocks ||
@@ -960,7 +969,7 @@ extern "C" int pa_select_blocks(const float* scores, int64_t score_stride, const
     if (num_rows < 0 || num_kv_heads <= 0 || max_context_len < 0 || block_size <= 0 || max_selected <= 0 ||
         num_first < 0 || num_last < 0 || (int64_t)num_first + num_last > max_selected)
         return PA_ERR_INVALID_ARG;
-    if (!supported_block_size(block_size)) return PA_ERR_UNSUPPORTED;
+    if (!supported_block_size(block_size) || num_rows > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     if (score_stride < ((int64_t)max_context_len + block_size - 1) / block_size) return PA_ERR_INVALID_ARG;
     if (num_rows == 0) return PA_OK;
     if (!scores || !context_lens || !selected || !aligned16(scores) || !aligned16(selected)) return PA_ERR_INVALID_ARG;

@@ -4,7 +4,9 @@
 // For each row r and query head h of kv head g, over the tokens t < L of the
 // blocks that selected[r][g] lists:
 //   out[r][h] = sum_t softmax(scale * <q[r][h], K_t>)_t V_t.
-// One pass with a running maximum and sum (log2 domain, fp32).
+// One pass with a running maximum and sum (log2 domain, fp32).  Bound by the
+// read of K and V: a block's tokens of one kv head are contiguous, blocks are
+// scattered.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -193,7 +195,11 @@ __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r,
 // matrix load touch all banks.
 // P is split into a bf16 value and a bf16 remainder (two products), so that
 // its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
-// once (2^-9) would be half of a bf16 output's own error.
+// once (2^-9) would be half of a bf16 output's own error.  (An infinite V meets a
+// remainder of the other sign, or zero, and gives NaN.)
+// Measured: 16 contexts, 64 / 8 heads of 128, 256 blocks of 16 tokens each (269
+// MB): 45.9 us, 5.85 TB/s, 0.89 of a copy, with one CTA on 128 of the 148 SMs;
+// 2048 lists of 64 blocks 157 us, 6.8 TB/s; one context of 128 blocks 6.1 us.
 // One cluster of `splits` CTAs per (row, kv head): its splits * WARPS warps take
 // the tiles of the list in turn, each with its own running maximum and sum, and
 // the states are joined through the cluster's shared memory, so that a long
@@ -396,7 +402,8 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) sparse_mma_kernel(cons
 // time: the products of 4 G scores are summed over the lanes by one
 // reduce-scatter (about 4 G shuffles instead of 4 G log2(D / 4)), so that each
 // weight is computed by one lane or few, and reaches the others through shared
-// memory.
+// memory.  Measured: 128 lists of 128 blocks of 16 tokens, D 128: one query head
+// 5.9 TB/s, eight 5.4 TB/s.
 template <int D, int G, int kStages>
 __global__ void __launch_bounds__(kF32Warps * 32, 1) sparse_f32_kernel(const SparseParams p, int splits) {
     constexpr int kLanes = D / 4;
@@ -652,7 +659,7 @@ extern "C" int pa_paged_attention_decode_sparse(const void* q, const void* k_poo
         !valid_dtype(out_dtype) || num_q_heads % num_kv_heads != 0)
         return PA_ERR_INVALID_ARG;
     if (!supported_head_dim(head_dim) || !supported_block_size(block_size) ||
-        !supported_group(num_q_heads / num_kv_heads, kv_dtype))
+        !supported_group(num_q_heads / num_kv_heads, kv_dtype) || num_rows > 0x7fffffff)
         return PA_ERR_UNSUPPORTED;
     if (!seq_ids && num_rows > batch) return PA_ERR_INVALID_ARG;
     if (num_rows == 0) return PA_OK;

@@ -56,6 +56,8 @@ def test_rope_refusals(lib, decode):
     assert bad(axes=3) == INVALID                    # several axes need pair_axes
     assert bad(maxpos=0) == INVALID                  # no table row
     assert bad(T=-1) == INVALID and bad(hq=0) == INVALID and bad(hkv=0) == INVALID
+    if not decode:
+        assert bad(T=1 << 40) == UNSUPPORTED
     if decode:
         assert bad(bt=0) == INVALID and bad(lens=0) == INVALID
         assert bad(pos=0, axes=3, pair=16) == INVALID
@@ -104,6 +106,7 @@ def test_scores_refusals(lib):
     assert _scores(lib, hq=6) == UNSUPPORTED         # group of 3
     assert _scores(lib, hq=32, dt=0) == UNSUPPORTED  # group of 16 needs bf16
     assert _scores(lib, d=96) == UNSUPPORTED and _scores(lib, bs=64) == UNSUPPORTED
+    assert _scores(lib, R=1 << 60, seq=16) == UNSUPPORTED
     assert _scores(lib, maxlen=-1) == INVALID and _scores(lib, dt=9) == INVALID
 
 
@@ -124,6 +127,7 @@ def test_select_refusals(lib):
     assert _select(lib, first=2**31 - 1, last=2**31 - 1) == INVALID
     assert _select(lib, stride=3) == INVALID
     assert _select(lib, bs=12) == UNSUPPORTED
+    assert _select(lib, R=1 << 60) == UNSUPPORTED
     assert _select(lib, hkv=0) == INVALID and _select(lib, R=-1) == INVALID
 
 
@@ -148,6 +152,7 @@ def test_sparse_decode_refusals(lib):
     assert _sparse(lib, hq=7) == INVALID and _sparse(lib, hq=6) == UNSUPPORTED
     assert _sparse(lib, hq=32, dt=0) == UNSUPPORTED
     assert _sparse(lib, d=80) == UNSUPPORTED and _sparse(lib, bs=1) == UNSUPPORTED
+    assert _sparse(lib, R=1 << 60, seq=16) == UNSUPPORTED
     assert _sparse(lib, odt=2) == INVALID and _sparse(lib, dt=2) == INVALID
 
 
