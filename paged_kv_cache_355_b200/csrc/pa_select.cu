@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
     constexpr int kOwn = BS / kRows;                          // rows of one lane
     constexpr int kBatch = kOwn < kPieceBytes / 512 ? kOwn : kPieceBytes / 512;  // of a piece
     constexpr int kPerHead = kOwn / kBatch;                   // pieces of one head
-    extern __shared__ __align__(16) uint8_t ring[];           // [warp][piece][row][lane]
+    extern __shared__ __align__(1024) uint8_t ring[];         // [warp][piece][row][lane]
     griddep_wait();
     griddep_launch_dependents();
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -851,20 +851,22 @@ int launch_scores(ScoreParams p, int head_dim, int dtype, cudaStream_t st) {
     const int64_t all = p.num_rows * p.num_kv_heads * tiles, sms = num_sms();
     // A CTA's warps take heads side by side: they share a row's look-ups, and a
     // row of one tile has work for all of them (256 rows of one tile, 8 kv
-    // heads: 4.4 us, against 7.1 with a head's tiles side by side).  Four tiles
-    // a warp once the grid has 32 warps an SM (16 contexts of 32k to 131k
-    // tokens: 77 us with one, 49 with four or eight; 256 of up to 4096: 18.5
-    // with one, 13.4 with four, 15.7 with eight).
+    // heads: 4.4 us, against 7.1 with a head's tiles side by side).  Up to
+    // four tiles a warp as long as that leaves 12 warps an SM (16 contexts of 32k
+    // to 131k tokens: 59 us with one, 50 with four or eight; 256 of up to 4096:
+    // 18.5 with one, 13.4 with four, 15.8 with eight; 256 of 700: 12.0 with one,
+    // 10.9 with three; 64 of 2000: 7.8 with two, 8.4 with one).
     p.head_warps = p.num_kv_heads > 2 ? kWarps : p.num_kv_heads;
     const int per_cta = kWarps / p.head_warps;  // tiles side by side
     p.parts = (p.num_kv_heads + p.head_warps - 1) / p.head_warps;
-    p.tiles_per_warp = (int)std::max((int64_t)1, std::min((int64_t)4, all / (sms * 32)));
+    p.tiles_per_warp = (int)std::max((int64_t)1, std::min((int64_t)4, all / (sms * 12)));
     p.chunks = (int)((tiles + per_cta * p.tiles_per_warp - 1) / (per_cta * p.tiles_per_warp));
-    // A ring of two tiles pays where most warps have several: rows of at most 16
-    // tiles are, in a ragged batch, mostly shorter, and better served by five
-    // CTAs an SM with one tile each than by three with two (256 rows of 700
-    // tokens: 10.8 against 12.5 us).
-    const bool brief = tiles <= 16 || p.tiles_per_warp == 1;
+    // A ring of two tiles pays only where all warps have several: 49.1 against
+    // 50.0 us for the 16 long contexts.  In a batch of shorter rows, ragged as a
+    // rule, most have fewer, and five CTAs an SM with one tile each do better
+    // than three with two (256 rows of up to 16k tokens: 31.0 against 34.6 us,
+    // of 700 tokens 10.9 against 12.5).
+    const bool brief = tiles <= 128 || p.tiles_per_warp == 1;
     const int group = p.num_q_heads / p.num_kv_heads;
     const bool wide = head_dim == 128;
     if (dtype == PA_BF16) {

@@ -189,6 +189,19 @@ def test_scores_of_a_long_row_among_short_ones(pa):
     assert pa.pa_read_error_flag() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 4), (64, 16)])
+def test_scores_of_many_long_rows(pa, dtype, d, group):
+    """Several tiles a warp, through the ring of two."""
+    if group == 16 and dtype == "f32":
+        pytest.skip("a group of 16 is bf16 only")
+    case, kb = score_inputs([30000, 17000], 2 * group, 2, d, 8, dtype, seed=7)
+    seqs = [0, 1, 0, 0, 1, 0, 0, 1, 0, 0, 0, 1]
+    lens = [30000, 17000, 29993, 1, 16391, 129, 0, 8192, 30000, 25000, 2049, 16999]
+    check_scores(pa, case, kb, 8, seqs=seqs, lens=lens)
+    assert pa.pa_read_error_flag() == 0
+
+
 def test_scores_bad_rows_and_special_values(pa):
     case, kb = score_inputs([64, 64], 4, 2, 64, 16, "bf16")
     tables = case.block_tables.clone()
