@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libpa.so.
+"""Thin ctypes binding of libpa.so (the shortest calls go through the C module
+_marshal instead of ctypes).
 
 Every function here has the name of the C entry point it calls and only
 marshals arguments: it reads shapes, dtypes and device pointers off torch
@@ -23,8 +24,8 @@ _STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_
            4: "PA_ERR_CUDA", 5: "PA_ERR_BAD_BLOCK_ID", 6: "PA_ERR_TIMEOUT"}
 _DTYPES = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m paged_kv_cache_355_b200.build` "
+if not all(os.path.exists(p) for p in (LIB_PATH, os.path.join(_HERE, "_marshal.so"))):
+    raise ImportError(f"{LIB_PATH} or _marshal.so is missing: build them with `python -m paged_kv_cache_355_b200.build` "
                       "(or __graft_entry__.build()); there is no fallback implementation")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -410,97 +411,100 @@ def pa_paged_attention_prefill(q, k_pool, v_pool, block_tables, context_lens, qu
         _kv_dtype(out), B, Hq, Hkv, D, T, NB, _kv_dtype(q), _stream(stream)))
 
 
-# The calls below take the device from their tensors: they run on it whichever
-# device is current, and refuse tensors of different devices.  They are short on
-# the device, so what they do on the host is kept short too: one test of each
-# tensor, and the stream handle without a Stream object around it.
-def _device_of(t, name: str) -> int:
+# The calls below are short on the device, so what they do on the host is kept
+# short too: the functions here compare shapes, and _marshal (a C module linked
+# with the same libpa.so) tests every tensor's device, type and layout on the way
+# to the entry point.  They run on their tensors' device, whichever is current.
+from . import _marshal  # noqa: E402  (libpa.so has to be loaded first)
+
+_ARG_NAMES = {
+    "pa_rope_and_cache": "query key value query_stride key_stride value_stride query_out k_pool v_pool slot_mapping "
+                         "positions num_axes pair_axes cos_sin max_position rotary_dim interleaved q_weight k_weight",
+    "pa_rope_and_cache_decode": "query key value query_stride key_stride value_stride query_out k_pool v_pool "
+                                "block_tables max_blocks_per_seq context_lens positions num_axes pair_axes cos_sin "
+                                "max_position rotary_dim interleaved q_weight k_weight eps batch num_q_heads "
+                                "num_kv_heads head_dim block_size num_blocks dtype slot_mapping",
+    "pa_update_key_bounds": "k_pool key_bounds block_tables max_blocks_per_seq context_lens query_start",
+    "pa_block_scores": "q key_bounds block_tables max_blocks_per_seq seq_ids context_lens max_context_len block_size "
+                       "scores",
+    "pa_select_blocks": "scores score_stride context_lens max_context_len block_size selected",
+    "pa_paged_attention_decode_sparse": "q k_pool v_pool block_tables max_blocks_per_seq seq_ids context_lens selected "
+                                        "max_selected scale block_size out",
+}
+_ENTRIES = _marshal.init(torch.int32, torch.int64, torch.float32)
+_ROPE, _ROPE_DECODE, _BOUNDS, _SCORES, _SELECT, _SPARSE = range(6)
+
+
+def _refuse(entry: int, index: int, device: int, dtype, args: tuple) -> None:
+    """Says what is wrong with the tensor args[index]."""
+    name, signature = _ENTRIES[entry]
+    what, t = _ARG_NAMES[name].split()[index], args[index]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-_Tensor = torch.Tensor
-
-
-def _on(t, name: str, dtype, device: int) -> int:
-    """Pointer of a contiguous tensor of this type on this device."""
-    if t.__class__ is _Tensor and t.get_device() == device and t.dtype is dtype and t.is_contiguous():
-        return t.data_ptr()
-    pointer = _dev(t, name, dtype)  # names what is wrong, or takes a subclass
+        raise TypeError(f"{what} must be a CUDA tensor")
+    want = {"i": torch.int32, "j": torch.int32, "l": torch.int64, "m": torch.int64, "f": torch.float32,
+            "o": t.dtype}.get(signature[index], dtype)
+    if t.dtype != want:
+        raise TypeError(f"{what} must be {want}, got {t.dtype}")
     if t.get_device() != device:
-        raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
-    return pointer
+        raise ValueError(f"tensors lie on different devices: {what} on {t.device}, the first on cuda:{device}")
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _opt(t, name: str, dtype, device: int):
-    return None if t is None else _on(t, name, dtype, device)
-
-
-def _call(name: str, device: int, stream, *args) -> None:
+def _raw_stream(stream, device: int) -> int:
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
-        raw = _stream(stream)
-    if device == torch.cuda.current_device():
-        status = getattr(_lib, name)(*args, raw)
+        return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
+    return _stream(stream)
+
+
+def _call(entry: int, device: int, dtype, args: tuple) -> None:
+    if device < 0 or device == torch.cuda.current_device():  # a tensor that is not on a GPU is refused by name
+        status = _marshal.call(entry, device, dtype, args)
     else:
         with torch.cuda.device(device):
-            status = getattr(_lib, name)(*args, raw)
-    if status != 0:
-        raise PAError(name, status)
+            status = _marshal.call(entry, device, dtype, args)
+    if status:
+        if status < 0:
+            _refuse(entry, -1 - status, device, dtype, args)
+        raise PAError(_ENTRIES[entry][0], status)
 
 
-def _token_rows(t, name: str, T: int, H: int, D: int, dtype, device: int) -> tuple[int, int]:
-    """Pointer and token stride of [tokens, heads, head_dim] rows whose tokens
-    may lie apart (a slice of one projection's output)."""
-    if t.get_device() != device or t.dtype is not dtype or t.shape != (T, H, D):
-        if _device_of(t, name) != device:
-            raise ValueError(f"tensors lie on different devices: {name} on {t.device}, the first on cuda:{device}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+def _token_stride(t, name: str, T: int, H: int, D: int) -> int:
+    """Elements between the tokens of [tokens, heads, head_dim] rows, which may
+    lie apart (a slice of one projection's output)."""
+    if t.shape != (T, H, D):
         raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
     st = t.stride()
     if st[2] != 1 or (H > 1 and st[1] != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st[0] if T > 1 else H * D)
+    return st[0] if T > 1 else H * D
 
 
-def _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, interleaved, q_weight,
-               k_weight, eps):
-    """Checks that both rotary calls share; returns the device, the sizes that
-    end the argument list, the arguments before the slots and those after."""
-    T, Hq, D = query.shape
-    NB, Hkv, bs, D2 = k_pool.shape
-    dtype = query.dtype
-    dt = _kv_dtype(query)
-    if D2 != D or v_pool.shape != k_pool.shape or query_out.shape != query.shape:
+def _rope_sizes(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, q_weight, k_weight):
+    """Checks that both rotary calls share; returns the tokens, the heads and
+    sizes, the three token strides, the axes and the shape of cos_sin."""
+    shape, pool = query.shape, k_pool.shape
+    T, Hq, D = shape
+    NB, Hkv, bs, D2 = pool
+    if D2 != D or v_pool.shape != pool or query_out.shape != shape:
         raise ValueError("query / query_out / pool shapes disagree")
-    device = _device_of(query, "query")
-    qp, qs = _token_rows(query, "query", T, Hq, D, dtype, device)
-    kp, ks = _token_rows(key, "key", T, Hkv, D, dtype, device)
-    vp, vs = _token_rows(value, "value", T, Hkv, D, dtype, device)
+    strides = (_token_stride(query, "query", T, Hq, D), _token_stride(key, "key", T, Hkv, D),
+               _token_stride(value, "value", T, Hkv, D))
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
     max_position, rotary_dim = cos_sin.shape
     axes = 1
     if positions is not None:
-        dims = positions.dim()
-        if dims not in (1, 2) or positions.shape[-1] != T:
+        pos = positions.shape
+        if len(pos) not in (1, 2) or pos[-1] != T:
             raise ValueError("positions must be [tokens] or [axes, tokens]")
-        axes = 1 if dims == 1 else positions.shape[0]
+        axes = 1 if len(pos) == 1 else pos[0]
     if pair_axes is not None and pair_axes.numel() != rotary_dim // 2:
         raise ValueError("pair_axes needs rotary_dim / 2 entries")
     if (q_weight is not None and q_weight.numel() != D) or (k_weight is not None and k_weight.numel() != D):
         raise ValueError("q_weight and k_weight need head_dim entries")
-    rows = (qp, kp, vp, qs, ks, vs, _on(query_out, "query_out", dtype, device), _on(k_pool, "k_pool", dtype, device),
-            _on(v_pool, "v_pool", dtype, device))
-    turn = (_opt(positions, "positions", torch.int32, device), axes, _opt(pair_axes, "pair_axes", torch.int32, device),
-            _on(cos_sin, "cos_sin", torch.float32, device), max_position, rotary_dim, 1 if interleaved else 0,
-            _opt(q_weight, "q_weight", dtype, device), _opt(k_weight, "k_weight", dtype, device), float(eps))
-    return device, (T, Hq, Hkv, D, bs, NB, dt), rows, turn
+    return T, Hq, Hkv, D, bs, NB, strides, axes, max_position, rotary_dim
 
 
 def pa_rope_and_cache(query, key, value, query_out, k_pool, v_pool, slot_mapping, positions, cos_sin, pair_axes=None,
@@ -510,12 +514,15 @@ def pa_rope_and_cache(query, key, value, query_out, k_pool, v_pool, slot_mapping
     heads; query_out gets the queries, the pools the keys and values at
     slot_mapping.  query, key and value may be slices of one projection's
     output ([tokens, heads, head_dim], tokens apart)."""
-    device, sizes, rows, turn = _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes,
-                                           interleaved, q_weight, k_weight, eps)
-    if slot_mapping.numel() != sizes[0] or positions is None:
+    T, Hq, Hkv, D, bs, NB, strides, axes, max_position, rotary_dim = _rope_sizes(
+        query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, q_weight, k_weight)
+    if slot_mapping.numel() != T or positions is None:
         raise ValueError("slot_mapping and positions need one entry a token")
-    _call("pa_rope_and_cache", device, stream, *rows, _on(slot_mapping, "slot_mapping", torch.int64, device), *turn,
-          *sizes)
+    device, dt = query.get_device(), _kv_dtype(query)
+    _call(_ROPE, device, query.dtype,
+          (query, key, value, *strides, query_out, k_pool, v_pool, slot_mapping, positions, axes, pair_axes, cos_sin,
+           max_position, rotary_dim, 1 if interleaved else 0, q_weight, k_weight, eps, T, Hq, Hkv, D, bs, NB, dt,
+           _raw_stream(stream, device)))
 
 
 def pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block_tables, context_lens, cos_sin,
@@ -524,16 +531,18 @@ def pa_rope_and_cache_decode(query, key, value, query_out, k_pool, v_pool, block
     """pa_rope_and_cache of one decode step: token b is position
     context_lens[b] - 1 of sequence b, its slot comes from the block table, and
     it turns by that position unless `positions` gives others."""
-    device, sizes, rows, turn = _rope_args(query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes,
-                                           interleaved, q_weight, k_weight, eps)
-    B, MBS = block_tables.shape
-    if B != sizes[0] or context_lens.numel() != B:
+    B, Hq, Hkv, D, bs, NB, strides, axes, max_position, rotary_dim = _rope_sizes(
+        query, key, value, query_out, k_pool, v_pool, positions, cos_sin, pair_axes, q_weight, k_weight)
+    rows, MBS = block_tables.shape
+    if rows != B or context_lens.numel() != B:
         raise ValueError("block_tables / context_lens do not match the batch of query")
     if slot_mapping is not None and slot_mapping.numel() != B:
         raise ValueError("slot_mapping needs one entry a sequence")
-    _call("pa_rope_and_cache_decode", device, stream, *rows, _on(block_tables, "block_tables", torch.int32, device), MBS,
-          _on(context_lens, "context_lens", torch.int32, device), *turn, *sizes,
-          _opt(slot_mapping, "slot_mapping", torch.int64, device))
+    device, dt = query.get_device(), _kv_dtype(query)
+    _call(_ROPE_DECODE, device, query.dtype,
+          (query, key, value, *strides, query_out, k_pool, v_pool, block_tables, MBS, context_lens, positions, axes,
+           pair_axes, cos_sin, max_position, rotary_dim, 1 if interleaved else 0, q_weight, k_weight, eps, B, Hq, Hkv,
+           D, bs, NB, dt, slot_mapping, _raw_stream(stream, device)))
 
 
 def pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, query_start=None, max_query_len: int = 1,
@@ -547,18 +556,15 @@ def pa_update_key_bounds(k_pool, key_bounds, block_tables, context_lens, query_s
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
     if context_lens.numel() != B or (query_start is not None and query_start.numel() != B + 1):
         raise ValueError("context_lens needs batch entries, query_start batch + 1")
-    dt, device = _kv_dtype(k_pool), _device_of(k_pool, "k_pool")
-    _call("pa_update_key_bounds", device, stream, _on(k_pool, "k_pool", k_pool.dtype, device),
-          _on(key_bounds, "key_bounds", k_pool.dtype, device), _on(block_tables, "block_tables", torch.int32, device),
-          MBS, _on(context_lens, "context_lens", torch.int32, device),
-          _opt(query_start, "query_start", torch.int32, device), int(max_query_len), B, Hkv, D, bs, NB, dt)
+    device, dt = k_pool.get_device(), _kv_dtype(k_pool)
+    _call(_BOUNDS, device, k_pool.dtype,
+          (k_pool, key_bounds, block_tables, MBS, context_lens, query_start, max_query_len, B, Hkv, D, bs, NB, dt,
+           _raw_stream(stream, device)))
 
 
-def _row_args(rows: int, block_tables, seq_ids, context_lens, device: int):
+def _check_rows(rows: int, seq_ids, context_lens) -> None:
     if context_lens.numel() != rows or (seq_ids is not None and seq_ids.numel() != rows):
         raise ValueError("context_lens and seq_ids need one entry a query row")
-    return (_on(block_tables, "block_tables", torch.int32, device), block_tables.shape[1],
-            _opt(seq_ids, "seq_ids", torch.int32, device), _on(context_lens, "context_lens", torch.int32, device))
 
 
 def pa_block_scores(q, key_bounds, block_tables, context_lens, max_context_len: int, block_size: int, scores,
@@ -568,13 +574,15 @@ def pa_block_scores(q, key_bounds, block_tables, context_lens, max_context_len: 
     [rows, Hkv, >= ceil(max_context_len / block_size)])."""
     R, Hq, D = q.shape
     NB, Hkv, two, D2 = key_bounds.shape
-    if D2 != D or two != 2 or scores.dim() != 3 or scores.shape[:2] != (R, Hkv):
+    B, MBS = block_tables.shape
+    out = scores.shape
+    if D2 != D or two != 2 or len(out) != 3 or out[0] != R or out[1] != Hkv:
         raise ValueError("q / key_bounds / scores shapes disagree")
-    dt, device = _kv_dtype(q), _device_of(q, "q")
-    _call("pa_block_scores", device, stream, _on(q, "q", q.dtype, device),
-          _on(key_bounds, "key_bounds", q.dtype, device), *_row_args(R, block_tables, seq_ids, context_lens, device),
-          int(max_context_len), int(block_size), _on(scores, "scores", torch.float32, device), scores.shape[2], R,
-          block_tables.shape[0], Hq, Hkv, D, NB, dt)
+    _check_rows(R, seq_ids, context_lens)
+    device, dt = q.get_device(), _kv_dtype(q)
+    _call(_SCORES, device, q.dtype,
+          (q, key_bounds, block_tables, MBS, seq_ids, context_lens, max_context_len, block_size, scores, out[2], R, B,
+           Hq, Hkv, D, NB, dt, _raw_stream(stream, device)))
 
 
 def pa_select_blocks(scores, context_lens, max_context_len: int, block_size: int, selected, num_first: int = 1,
@@ -583,28 +591,29 @@ def pa_select_blocks(scores, context_lens, max_context_len: int, block_size: int
     num_first and last num_last blocks and those of the largest score, in
     ascending order, -1 behind them."""
     R, Hkv, S = scores.shape
-    if selected.dim() != 3 or selected.shape[:2] != (R, Hkv) or context_lens.numel() != R:
+    out = selected.shape
+    if len(out) != 3 or out[0] != R or out[1] != Hkv or context_lens.numel() != R:
         raise ValueError("scores / selected / context_lens shapes disagree")
-    device = _device_of(scores, "scores")
-    _call("pa_select_blocks", device, stream, _on(scores, "scores", torch.float32, device), S,
-          _on(context_lens, "context_lens", torch.int32, device), int(max_context_len), int(block_size),
-          _on(selected, "selected", torch.int32, device), selected.shape[2], int(num_first), int(num_last), R, Hkv)
+    device = scores.get_device()
+    _call(_SELECT, device, None,
+          (scores, S, context_lens, max_context_len, block_size, selected, out[2], num_first, num_last, R, Hkv,
+           _raw_stream(stream, device)))
 
 
 def pa_paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens, selected, scale: float, out,
                                      seq_ids=None, stream=None) -> None:
     """Decode attention of each row over the tokens of the blocks that
     selected[r, g] lists (negative entries name no block)."""
-    R, Hq, D = q.shape
-    NB, Hkv, bs, D2 = k_pool.shape
-    if D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape:
+    shape, pool, listed = q.shape, k_pool.shape, selected.shape
+    R, Hq, D = shape
+    NB, Hkv, bs, D2 = pool
+    B, MBS = block_tables.shape
+    if D2 != D or v_pool.shape != pool or out.shape != shape:
         raise ValueError("q / pool / out shapes disagree")
-    if selected.dim() != 3 or selected.shape[:2] != (R, Hkv):
+    if len(listed) != 3 or listed[0] != R or listed[1] != Hkv:
         raise ValueError("selected must be [rows, num_kv_heads, max_selected]")
-    dtype, dt, out_dt = q.dtype, _kv_dtype(q), _kv_dtype(out)
-    device = _device_of(q, "q")
-    _call("pa_paged_attention_decode_sparse", device, stream, _on(q, "q", dtype, device),
-          _on(k_pool, "k_pool", dtype, device), _on(v_pool, "v_pool", dtype, device),
-          *_row_args(R, block_tables, seq_ids, context_lens, device), _on(selected, "selected", torch.int32, device),
-          selected.shape[2], float(scale), bs, _on(out, "out", out.dtype, device), out_dt, R, block_tables.shape[0], Hq, Hkv, D,
-          NB, dt)
+    _check_rows(R, seq_ids, context_lens)
+    device, dt, out_dt = q.get_device(), _kv_dtype(q), _kv_dtype(out)
+    _call(_SPARSE, device, q.dtype,
+          (q, k_pool, v_pool, block_tables, MBS, seq_ids, context_lens, selected, listed[2], scale, bs, out, out_dt, R,
+           B, Hq, Hkv, D, NB, dt, _raw_stream(stream, device)))

@@ -182,3 +182,39 @@ def test_binding_names_what_is_wrong():
         pa.pa_paged_attention_decode_sparse(q, pool, pool, tables, lens, z(3, 4, 2, dtype=i32), 0.1, q)
     with pytest.raises(TypeError, match="must be a CUDA tensor"):
         pa.pa_paged_attention_decode_sparse(q, pool, pool, tables, lens, z(3, 2, 2, dtype=i32), 0.1, q)
+
+
+def test_marshalling_signatures_are_the_entry_points():
+    """The C module's letters, argument by argument, against the ctypes types,
+    and a name for every tensor it may refuse."""
+    from paged_kv_cache_355_b200 import _binding as b
+
+    scalar = {"I": b._I, "L": b._I64, "F": b._F}
+    assert len(b._ENTRIES) == 6
+    for name, signature in b._ENTRIES:
+        types, _ = b._SIGS[name]
+        assert [scalar.get(c, b._P) for c in signature] == types, name
+        names = b._ARG_NAMES[name].split()
+        assert all(i < len(names) for i, c in enumerate(signature) if c in "KilforkjmR"), name
+    order = (b._ROPE, b._ROPE_DECODE, b._BOUNDS, b._SCORES, b._SELECT, b._SPARSE)
+    assert [b._ENTRIES[i][0] for i in order] == [
+        "pa_rope_and_cache", "pa_rope_and_cache_decode", "pa_update_key_bounds", "pa_block_scores", "pa_select_blocks",
+        "pa_paged_attention_decode_sparse"]
+
+
+def test_marshalling_refuses():
+    from paged_kv_cache_355_b200 import _binding as b
+
+    call = b._marshal.call
+    with pytest.raises(TypeError, match="wrong number of arguments"):
+        call(b._SELECT, 0, None, ())
+    with pytest.raises(ValueError, match="no such entry point"):
+        call(6, 0, None, ())
+    with pytest.raises(ValueError, match="no such entry point"):
+        call(-1, 0, None, ())
+    with pytest.raises(TypeError):
+        call(b._SELECT, 0, None, [])
+    # what is no tensor, or a tensor on the CPU, is refused by its place
+    for t in (None, 3, "x", torch.zeros(2)):
+        assert call(b._SELECT, 0, None, (t,) * 12) == -1
+        assert call(b._SELECT, -1, None, (t,) * 12) == -1

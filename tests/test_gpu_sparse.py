@@ -272,6 +272,27 @@ def test_select_long_rows(pa, S):
     assert pa.pa_read_error_flag() == 0
 
 
+def test_arguments_of_the_wrong_kind(pa):
+    """Refused by name before anything runs; numbers may be anything that counts."""
+    scores, lens = torch.zeros(2, 1, 5, device="cuda"), i32([40, 33]).cuda()
+    out = torch.full((2, 1, 4), 7, dtype=torch.int32, device="cuda")
+    for bad, kind, what in (((scores.double(), lens, 40, 8, out), TypeError, "scores must be torch.float32"),
+                            ((scores, lens.long(), 40, 8, out), TypeError, "context_lens must be torch.int32"),
+                            ((scores, lens.cpu(), 40, 8, out), TypeError, "context_lens must be a CUDA tensor"),
+                            ((scores, lens, 40, 8, out.transpose(0, 2).contiguous().transpose(0, 2)), ValueError,
+                             "selected must be contiguous"),
+                            ((scores, lens, 1 << 40, 8, out), OverflowError, "out of range"),
+                            ((scores, lens, "40", 8, out), TypeError, "integer")):
+        with pytest.raises(kind, match=what):
+            pa.pa_select_blocks(*bad)
+    with pytest.raises(TypeError):
+        pa.pa_select_blocks(scores, lens, 40.5, 8, out)
+    assert (out == 7).all()
+    pa.pa_select_blocks(torch.nn.Parameter(scores), lens, np.int64(40), torch.tensor(8), out)
+    assert out[:, 0].tolist() == [[0, 1, 3, 4]] * 2
+    assert pa.pa_read_error_flag() == 0
+
+
 def test_select_bad_lengths(pa):
     scores = torch.randn(3, 2, 10)
     got = torch.full((3, 2, 4), 99, dtype=torch.int32, device="cuda")
