@@ -580,14 +580,13 @@ __device__ __forceinline__ uint32_t max_lanes(uint32_t x) { return __reduce_max_
 
 // The row of one (row, kv head) as the selection sees it.
 struct SelectRow {
-    const float* scores;
     int32_t* out;
     int blocks;      // of the row
     int last;        // the first of its last num_last blocks
     int num_first, want;  // want: blocks to choose besides the first and last
     __device__ __forceinline__ bool always(int j) const { return j < num_first || j >= last; }
-    __device__ __forceinline__ uint32_t key(int j) const {
-        return j < blocks && !always(j) ? score_key(scores[j]) : 0u;
+    __device__ __forceinline__ uint32_t key(int j, float score) const {
+        return j < blocks && !always(j) ? score_key(score) : 0u;
     }
 };
 
@@ -607,18 +606,17 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int64_t unit, 
         for (int i = thread; i < p.max_selected; i += threads) r.out[i] = i < r.blocks ? i : -1;
         return false;
     }
-    r.scores = p.scores + unit * p.score_stride;
     r.num_first = p.num_first;
     r.last = r.blocks - p.num_last;
     r.want = p.max_selected - p.num_first - p.num_last;
     return true;
 }
 
-// Short rows, at most 32 * kItems blocks: one warp a row, its keys in
+// Short rows, at most 32 * kShortItems blocks: one warp a row, its keys in
 // registers.  The value of the last key to be taken is found by bisection, a
 // count over the warp a step, which ends early at any value that exactly
 // max_selected keys reach.  Bound by latency: 2048 rows of up to 256 blocks, 64
-// kept, 6.3 us.
+// kept, 5.3 us.
 constexpr int kShortItems = 8;
 
 __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectParams p) {
@@ -627,12 +625,17 @@ __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectP
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (unit >= p.num_rows * p.num_kv_heads) return;
     const int lane = threadIdx.x & 31;
+    // the scores are read beside the row's length, whether or not it is that long
+    const float* scores = p.scores + unit * p.score_stride;
+    float score[kShortItems];
+#pragma unroll
+    for (int i = 0; i < kShortItems; ++i) score[i] = 32 * i + lane < p.score_stride ? scores[32 * i + lane] : 0.f;
     SelectRow r;
     if (!select_row(p, unit, lane, 32, r)) return;
     uint32_t key[kShortItems], lo = 0xffffffffu, hi = 0;
 #pragma unroll
     for (int i = 0; i < kShortItems; ++i) {
-        key[i] = r.key(32 * i + lane);
+        key[i] = r.key(32 * i + lane, score[i]);
         hi = max(hi, key[i]);
         if (key[i]) lo = min(lo, key[i]);
     }
@@ -683,11 +686,10 @@ __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectP
 // would all be the same (and the counters' atomics would collide).  Counts are
 // integers: the order of the atomics changes nothing.  Rows of up to THREADS *
 // kItems blocks are read once, longer ones once a pass.  Bound by latency and
-// barriers: 128 rows of 2048 to 8192 blocks, 256 kept, 8.6 us.
+// barriers: 128 rows of 2048 to 8192 blocks, 256 kept, 7.6 us.
 constexpr int kBins = 2048;
-constexpr int kItems = 8;
 
-template <int THREADS>
+template <int THREADS, int kItems>
 __global__ void __launch_bounds__(THREADS) select_long_kernel(const SelectParams p) {
     constexpr int kW = THREADS / 32;
     constexpr int kOwn = kBins / THREADS;  // bins of one thread
@@ -698,15 +700,27 @@ __global__ void __launch_bounds__(THREADS) select_long_kernel(const SelectParams
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // warp w's part of a chunk is contiguous, item i its i-th 32 blocks; the first
+    // chunk is read beside the row's length, whether or not it is that long
+    const float* scores = p.scores + blockIdx.x * p.score_stride;
+    auto first_of = [&](int chunk) { return chunk * THREADS * kItems + warp * 32 * kItems + lane; };
+    float score[kItems];
+    auto read = [&](int chunk) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int j = first_of(chunk) + 32 * i;
+            score[i] = j < p.score_stride ? scores[j] : 0.f;
+        }
+    };
+    read(0);
     SelectRow r;
     if (!select_row(p, blockIdx.x, tid, THREADS, r)) return;
     const int chunks = (r.blocks + THREADS * kItems - 1) / (THREADS * kItems);
     uint32_t key[kItems];
-    // warp w's part of a chunk is contiguous, item i its i-th 32 blocks
-    auto first_of = [&](int chunk) { return chunk * THREADS * kItems + warp * 32 * kItems + lane; };
     auto load = [&](int chunk) {
+        if (chunk > 0 || chunks > 1) read(chunk);
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) key[i] = r.key(first_of(chunk) + 32 * i);
+        for (int i = 0; i < kItems; ++i) key[i] = r.key(first_of(chunk) + 32 * i, score[i]);
     };
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) hist[tid * kOwn + i] = 0;
@@ -993,10 +1007,12 @@ extern "C" int pa_select_blocks(const float* scores, int64_t score_stride, const
     if (!p.err) return PA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // by the longest row that may come: a warp a row while its keys fit the
-    // warp's registers, then a CTA of 256 threads, or of 1024
+    // warp's registers, then a CTA of 512 threads with four blocks each (512 rows
+    // of up to 1000 blocks: 9.9 us, with 256 threads 10.3, with 1024 14.0), or of
+    // 1024 with eight (128 rows of 2048 to 8192 blocks: 7.6 us, 8.1 with 512)
     const int64_t blocks = ((int64_t)max_context_len + block_size - 1) / block_size;
     if (blocks <= 32 * kShortItems)
         return launch_pdl(select_short_kernel, dim3((unsigned)((grid + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, p);
-    if (blocks <= 256 * kItems) return launch_pdl(select_long_kernel<256>, dim3((unsigned)grid), dim3(256), 0, st, p);
-    return launch_pdl(select_long_kernel<1024>, dim3((unsigned)grid), dim3(1024), 0, st, p);
+    if (blocks <= 2048) return launch_pdl(select_long_kernel<512, 4>, dim3((unsigned)grid), dim3(512), 0, st, p);
+    return launch_pdl(select_long_kernel<1024, 8>, dim3((unsigned)grid), dim3(1024), 0, st, p);
 }

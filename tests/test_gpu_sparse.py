@@ -241,7 +241,7 @@ def check_select(pa, scores, lens, bs, K, first, last, max_len=None):
 
 @pytest.mark.parametrize("kind", ["normal", "grid", "equal", "special", "ascending"])
 @pytest.mark.parametrize("K,first,last", [(1, 0, 0), (1, 0, 1), (5, 1, 2), (64, 1, 2), (64, 64, 0), (200, 1, 1)])
-@pytest.mark.parametrize("S", [200, 331, 2100])  # a warp, 256 and 1024 threads a row
+@pytest.mark.parametrize("S", [200, 331, 2100])  # a warp, 512 and 1024 threads a row
 def test_select(pa, kind, K, first, last, S):
     bs, R, hkv = 8, 9, 3
     g = torch.Generator().manual_seed(K)
