@@ -156,7 +156,7 @@ def test_sparse_decode_refusals(lib):
     assert _sparse(lib, odt=2) == INVALID and _sparse(lib, dt=2) == INVALID
 
 
-def test_binding_names_what_is_wrong():
+def test_binding_names_what_is_wrong(lib):
     """Shapes, layouts, types and places that the binding refuses by name."""
     import paged_kv_cache_355_b200 as pa
 
@@ -184,7 +184,7 @@ def test_binding_names_what_is_wrong():
         pa.pa_paged_attention_decode_sparse(q, pool, pool, tables, lens, z(3, 2, 2, dtype=i32), 0.1, q)
 
 
-def test_marshalling_signatures_are_the_entry_points():
+def test_marshalling_signatures_are_the_entry_points(lib):
     """The C module's letters, argument by argument, against the ctypes types,
     and a name for every tensor it may refuse."""
     from paged_kv_cache_355_b200 import _binding as b
@@ -202,7 +202,7 @@ def test_marshalling_signatures_are_the_entry_points():
         "pa_paged_attention_decode_sparse"]
 
 
-def test_marshalling_refuses():
+def test_marshalling_refuses(lib):
     from paged_kv_cache_355_b200 import _binding as b
 
     call = b._marshal.call

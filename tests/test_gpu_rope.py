@@ -111,7 +111,7 @@ def test_prompt_rows(pa, dtype, d, rotary, interleaved, norm):
     assert pa.pa_read_error_flag() == 0
 
 
-@pytest.mark.parametrize("tokens,hq,hkv", [(1, 1, 1), (1, 32, 8), (3, 5, 5), (2, 7, 1), (64, 16, 4), (700, 12, 4)])
+@pytest.mark.parametrize("tokens,hq,hkv", [(1, 1, 1), (1, 32, 8), (3, 5, 5), (2, 7, 1), (64, 14, 4), (700, 12, 4)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("bs", [8, 32])
 def test_head_counts_and_lengths(pa, tokens, hq, hkv, dtype, bs):
