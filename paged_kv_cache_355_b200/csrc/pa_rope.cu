@@ -18,7 +18,7 @@
 // of the rotated part.
 // Measured on one B200: 24,175 prompt tokens of 64 / 8 heads of 128, bf16, both
 // norms, three axes (995 MB): 157 us, 6.35 TB/s, 0.97 of a copy; 4,582 tokens
-// of 32 / 32 heads, half rotated, neighbours (226 MB): 37.8 us, 5.97 TB/s; a
+// of 32 / 32 heads, half rotated, neighbours (226 MB): 37.5 us, 6.0 TB/s; a
 // decode step of 256 sequences, 32 / 8 heads (6.4 MB): 3.5 us, a chain of three
 // dependent loads.
 #include <cuda_bf16.h>
@@ -107,7 +107,12 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             to[u] = Chunk<T>{};
-            if (head + u * kHeads < limit) to[u].load(src + u * kHeads * D, src + u * kHeads * D + other);
+            if (head + u * kHeads < limit) {
+                if (NEIGHBOURS)
+                    to[u].load(src + u * kHeads * D);
+                else
+                    to[u].load(src + u * kHeads * D, src + u * kHeads * D + other);
+            }
         }
     };
     load(rows, first);  // beside the look-up of where they go
@@ -230,7 +235,12 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
                 }
                 rows[u].from_f32(y);
             }
-            if (head + u * kHeads + sub < limit) rows[u].store(dst, dst + other);
+            if (head + u * kHeads + sub < limit) {
+                if (NEIGHBOURS)
+                    rows[u].store(dst);
+                else
+                    rows[u].store(dst, dst + other);
+            }
             dst += dst_step;
         }
 #pragma unroll

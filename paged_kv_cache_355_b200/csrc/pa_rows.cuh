@@ -1,6 +1,6 @@
-// pa_rows.cuh -- head rows in registers: one lane holds 8 consecutive
-// elements of a row of head_dim elements, so head_dim / 8 lanes hold a row.
-// bf16 chunks are one 16-byte vector, fp32 chunks two.
+// pa_rows.cuh -- helpers of the kernels that take rows of head_dim elements
+// apart over a warp's lanes: chunks of 8 elements, sums over lanes, asynchronous
+// copies to shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
