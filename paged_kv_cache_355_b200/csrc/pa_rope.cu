@@ -117,40 +117,41 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
     };
     load(rows, first);  // beside the look-up of where they go
 
-    // where the token goes
-    int64_t slot = -1, text_pos = -1;
-    bool bad = false;
+    // where the token goes: looked up here, looked at after the angles, so that
+    // the two chains of loads run side by side
+    const int shift = block_shift(p.block_size);
+    int64_t text_pos = -1, place;  // the slot, or the block table's entry
     if (DECODE) {
-        const int L = p.context_lens[token];
-        if (L > 0) {
-            text_pos = L - 1;
-            const int64_t j = text_pos / p.block_size;
-            int64_t blk = -1;
-            if (j < p.max_blocks_per_seq) blk = p.block_tables[token * p.max_blocks_per_seq + j];
-            if (blk >= 0 && blk < p.num_blocks) slot = blk * p.block_size + text_pos % p.block_size;
-        }
-        bad = L != 0 && slot < 0;
+        text_pos = (int64_t)p.context_lens[token] - 1;
+        const int64_t j = text_pos >> shift;
+        place = text_pos >= 0 && j < p.max_blocks_per_seq ? p.block_tables[token * p.max_blocks_per_seq + j] : -1;
     } else {
-        slot = p.slot_mapping[token];
-        bad = slot >= p.num_blocks * p.block_size;
+        place = p.slot_mapping[token];
     }
-    // its angles, a pair or two a lane; a bad position or axis reads nothing
+    // the token's angles, a pair or two a lane; a bad position or axis reads nothing
     const int half = p.rotary_dim / 2;
-    if (DECODE ? text_pos >= 0 : slot >= 0) {
+    bool bad = false;
 #pragma unroll
-        for (int i = 0; i < D / 2; i += 32) {
-            const int pair = i + lane;
-            if (pair >= half) break;
-            const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
-            int64_t pos = text_pos;
-            if (p.positions) pos = axis >= 0 && axis < p.num_axes ? (int64_t)p.positions[(int64_t)axis * p.num_tokens + token] : -1;
-            if (pos >= 0 && pos < p.max_position) {
-                cs[0][pair] = p.cos_sin[pos * p.rotary_dim + pair];
-                cs[1][pair] = p.cos_sin[pos * p.rotary_dim + half + pair];
-            } else {
-                bad = true;
-            }
+    for (int i = 0; i < D / 2; i += 32) {
+        const int pair = i + lane;
+        if (pair >= half) break;
+        const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
+        int64_t pos = text_pos;
+        if (p.positions) pos = axis >= 0 && axis < p.num_axes ? (int64_t)p.positions[(int64_t)axis * p.num_tokens + token] : -1;
+        if (pos >= 0 && pos < p.max_position) {
+            cs[0][pair] = p.cos_sin[pos * p.rotary_dim + pair];
+            cs[1][pair] = p.cos_sin[pos * p.rotary_dim + half + pair];
+        } else {
+            bad = true;
         }
+    }
+    int64_t slot = -1;
+    if (DECODE) {
+        if (place >= 0 && place < p.num_blocks) slot = (place << shift) + (text_pos & (p.block_size - 1));
+        bad = text_pos != -1 && (bad || slot < 0);  // a length of 0 is an empty sequence
+    } else {
+        slot = place;
+        bad = slot >= 0 && (bad || slot >= p.num_blocks << shift);  // a negative slot is padding
     }
     bad = __any_sync(0xffffffffu, bad);
     const bool write = slot >= 0 && !bad;
@@ -186,8 +187,8 @@ __global__ void __launch_bounds__(32, 24) rope_cache_kernel(const RopeParams p) 
             f[3][i] = w1 * s[i];
         }
     };
-    const int64_t blk = slot / p.block_size;
-    const int off = (int)(slot - blk * p.block_size);
+    const int64_t blk = slot >> shift;
+    const int off = (int)slot & (p.block_size - 1);
     T* q_dst = static_cast<T*>(p.query_out) + token * Hq * D;
     const int64_t pool_row = ((blk * Hkv) * p.block_size + off) * D;  // kv head 0
     T* k_dst = static_cast<T*>(p.k_pool) + pool_row;

@@ -70,6 +70,10 @@ struct Chunk<float> {
     }
 };
 
+// log2 of a block size (8, 16 or 32): 64-bit divisions by it are a hundred
+// cycles of a chain that takes a few thousand.
+__device__ __forceinline__ int block_shift(int block_size) { return __popc(block_size - 1); }
+
 // Minimum and maximum that keep a NaN of either side.
 __device__ __forceinline__ float min_nan(float x, float y) {
     float r;

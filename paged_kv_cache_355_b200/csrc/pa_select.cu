@@ -305,7 +305,7 @@ __device__ __forceinline__ void end_tiles(const ScoreParams& p, WarpTiles& w) {
     if (!w.named || L < 0 || L > p.max_context_len) {
         if (w.recorder) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
     } else {
-        w.blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
+        w.blocks = (int)(((int64_t)L + p.block_size - 1) >> block_shift(p.block_size));
     }
     w.end = min(w.end, (w.blocks + 15) / 16);
 }
@@ -361,7 +361,7 @@ struct Entries {
 // products are exact: a matrix product (m16n8k16) of 16 blocks with the group's
 // heads, padded to 8 by repeats, which leave the maximum alone.  Bound by the
 // read of the bounds: a block's two rows are 4 D contiguous bytes, copied
-// asynchronously into a ring of two tiles that belongs to the warp alone.
+// asynchronously into a ring of one or two tiles that belongs to the warp alone.
 // 16-byte chunk c of block b lies at c ^ (b & 7), so that the eight rows of a
 // matrix load touch all banks.
 // Measured: 16 contexts of 32k to 131k tokens, 64 / 8 heads of 128 (313 MB): 49
@@ -600,7 +600,7 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int64_t unit, 
     if (L < 0 || L > p.max_context_len) {
         if (unit == row * p.num_kv_heads && thread == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
     } else {
-        r.blocks = (int)(((int64_t)L + p.block_size - 1) / p.block_size);
+        r.blocks = (int)(((int64_t)L + p.block_size - 1) >> block_shift(p.block_size));
     }
     if (r.blocks <= p.max_selected) {
         for (int i = thread; i < p.max_selected; i += threads) r.out[i] = i < r.blocks ? i : -1;
