@@ -17,10 +17,10 @@
 // holds 8 elements, both elements of four pairs: 8 neighbours, or 4 of each half
 // of the rotated part.
 // Measured on one B200: 24,175 prompt tokens of 64 / 8 heads of 128, bf16, both
-// norms, three axes (995 MB): 157 us, 6.35 TB/s, 0.97 of a copy; 4,582 tokens
-// of 32 / 32 heads, half rotated, neighbours (226 MB): 37.5 us, 6.0 TB/s; a
-// decode step of 256 sequences, 32 / 8 heads (6.4 MB): 3.5 us, a chain of three
-// dependent loads.
+// norms, three axes (995 MB): 156 us, 6.4 TB/s, 0.97 of a copy; 4,582 tokens of
+// 32 / 32 heads, half rotated, neighbours (226 MB): 37.2 us, 6.1 TB/s; a decode
+// step of 256 sequences, 32 / 8 heads (6.4 MB): 3.2 us, two dependent loads and
+// the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

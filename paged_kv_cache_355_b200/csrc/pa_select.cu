@@ -38,7 +38,7 @@ struct BoundsParams {
     int max_query_len, batch, num_kv_heads, block_size;
     int64_t num_blocks;
     int max_touched;  // blocks that max_query_len new tokens can lie in
-    int heads_per_warp;
+    int heads_per_warp, parts;  // parts: warps for a block's heads
     int* err;
 };
 
@@ -143,14 +143,12 @@ __global__ void __launch_bounds__(kWarps * 32) key_bounds_kernel(const BoundsPar
     extern __shared__ __align__(1024) uint8_t ring[];         // [warp][piece][row][lane]
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int parts = (p.num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp;
-    const int64_t per_seq = (int64_t)p.max_touched * parts;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t per_seq = (uint32_t)p.max_touched * p.parts;
     const int64_t b = unit / per_seq;
     if (b >= p.batch) return;
-    const int64_t rem = unit - b * per_seq;
-    const int i = (int)(rem / parts);
-    const int part = (int)(rem - (int64_t)i * parts);
+    const uint32_t rem = unit % per_seq;
+    const int i = (int)(rem / p.parts), part = (int)(rem % p.parts);
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, chunk = lane % kLanes;
 
@@ -227,10 +225,11 @@ int launch_bounds(BoundsParams p, cudaStream_t st) {
     // a warp takes as many kv heads of a block as leave 64 warps an SM
     const int64_t all = (int64_t)p.batch * p.max_touched * p.num_kv_heads;
     const int64_t heads = std::max((int64_t)1, std::min((int64_t)p.num_kv_heads, all / ((int64_t)num_sms() * 64)));
-    const int64_t parts = (p.num_kv_heads + heads - 1) / heads;
-    p.heads_per_warp = (int)((p.num_kv_heads + parts - 1) / parts);
-    const int64_t blocks = ((int64_t)p.batch * p.max_touched * parts + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    p.parts = (int)((p.num_kv_heads + heads - 1) / heads);
+    p.heads_per_warp = (p.num_kv_heads + p.parts - 1) / p.parts;
+    const int64_t per_seq = (int64_t)p.max_touched * p.parts;
+    if (per_seq > 0x7fffffff / p.batch) return PA_ERR_UNSUPPORTED;  // warps are counted in 32 bits
+    const int64_t blocks = (p.batch * per_seq + kWarps - 1) / kWarps;
     auto kernel = p.block_size == 8    ? key_bounds_kernel<T, D, 8>
                   : p.block_size == 16 ? key_bounds_kernel<T, D, 16>
                                        : key_bounds_kernel<T, D, 32>;
@@ -279,10 +278,10 @@ struct WarpTiles {
 // Where the warp is, without the row's length: its table may be read beside it.
 __device__ __forceinline__ WarpTiles warp_tiles(const ScoreParams& p) {
     WarpTiles w;
-    const int64_t unit = blockIdx.x / p.chunks;
-    const int chunk = (int)(blockIdx.x - unit * p.chunks), warp = threadIdx.x >> 5;
+    const uint32_t unit = blockIdx.x / p.chunks;
+    const int chunk = (int)(blockIdx.x % p.chunks), warp = threadIdx.x >> 5;
     w.row = unit / p.parts;
-    w.h = (int)(unit - w.row * p.parts) * p.head_warps + (warp & (p.head_warps - 1));
+    w.h = (int)(unit % p.parts) * p.head_warps + (warp & (p.head_warps - 1));
     const int64_t seq = p.seq_ids ? (int64_t)p.seq_ids[w.row] : w.row;
     w.named = seq >= 0 && seq < p.batch;
     w.recorder = chunk == 0 && w.h == 0 && threadIdx.x == 0;
@@ -592,10 +591,10 @@ struct SelectRow {
 
 // False where the row is already written: no more blocks than max_selected
 // (all of them), or a bad length (none).  Called by `threads` threads.
-__device__ __forceinline__ bool select_row(const SelectParams& p, int64_t unit, int thread, int threads, SelectRow& r) {
-    const int64_t row = unit / p.num_kv_heads;
+__device__ __forceinline__ bool select_row(const SelectParams& p, uint32_t unit, int thread, int threads, SelectRow& r) {
+    const uint32_t row = unit / p.num_kv_heads;
     const int L = p.context_lens[row];
-    r.out = p.selected + unit * p.max_selected;
+    r.out = p.selected + (int64_t)unit * p.max_selected;
     r.blocks = 0;
     if (L < 0 || L > p.max_context_len) {
         if (unit == row * p.num_kv_heads && thread == 0) record_error(p.err, PA_ERR_BAD_BLOCK_ID);
@@ -622,7 +621,7 @@ constexpr int kShortItems = 8;
 __global__ void __launch_bounds__(kWarps * 32) select_short_kernel(const SelectParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (unit >= p.num_rows * p.num_kv_heads) return;
     const int lane = threadIdx.x & 31;
     // the scores are read beside the row's length, whether or not it is that long

@@ -91,9 +91,10 @@ struct Row {
 
     // Reads the list's entry of half-tile `half` beside the row's length.
     __device__ __forceinline__ int open(const SparseParams& p, int splits, int64_t half, int64_t halves, int shift) {
-        unit = blockIdx.x / splits;
-        row = unit / p.num_kv_heads;
-        h = (int)(unit - row * p.num_kv_heads);
+        const uint32_t u = blockIdx.x / splits;
+        unit = u;
+        row = u / p.num_kv_heads;
+        h = (int)(u % p.num_kv_heads);
         group = p.num_q_heads / p.num_kv_heads;
         list = p.selected + unit * p.max_selected;
         const int entry = half < halves ? list[half >> shift] : -1;
