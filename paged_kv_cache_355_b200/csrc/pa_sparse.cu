@@ -194,13 +194,19 @@ __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r,
 // accumulator, rounded and transposed in 8x8 matrices between the lanes.
 // 16-byte chunk c of a row lies at c ^ (row & 7), so that the eight rows of a
 // matrix load touch all banks.
-// P is split into a bf16 value and a bf16 remainder (two products), so that
-// its rounding, 2^-17 of P, stays far below the fp32 output's use; rounding P
-// once (2^-9) would be half of a bf16 output's own error.  (An infinite V meets a
-// remainder of the other sign, or zero, and gives NaN.)
+// P enters its product in 32 bits: as a bf16 value and two bf16 remainders (three
+// products; rounded once it is off by 2^-8, with one remainder by 2^-17), and each
+// tile's products are summed by themselves, smallest first, and added to the
+// running output by rounded additions, since the matrix instruction cuts off what
+// does not fit its sum: through a running sum of 43 tiles a warp, an fp32 output was
+// 2.9e-6 (relative, in norm) below the definition, and is 2.5e-7 off it now, as in
+// the fp32 kernel.  This costs 1 % on streams of long lists (45.7 to 46.3 us), 5 %
+// on one context (6.1 to 6.4 us), 7 % with a group of 16 (51.0 to 54.5 us).
+// (An infinite V meets a remainder of the other sign, or zero, and gives NaN.)
 // Measured: 16 contexts, 64 / 8 heads of 128, 256 blocks of 16 tokens each (269
-// MB): 45.9 us, 5.85 TB/s, 0.89 of a copy, with one CTA on 128 of the 148 SMs;
-// 2048 lists of 64 blocks 157 us, 6.8 TB/s; one context of 128 blocks 6.1 us.
+// MB): 46.3 us, 5.80 TB/s, 0.88 of a copy, with one CTA on 128 of the 148 SMs;
+// 2048 lists of 64 blocks 160 us, 6.7 TB/s; one context of 128 blocks 6.4 us; a
+// group of 16, 128 lists of 256 blocks, 4.9 TB/s.
 // One cluster of `splits` CTAs per (row, kv head): its splits * WARPS warps take
 // the tiles of the list in turn, each with its own running maximum and sum, and
 // the states are joined through the cluster's shared memory, so that a long
@@ -339,28 +345,34 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) sparse_mma_kernel(cons
                         }
                     }
             }
-            uint32_t hi[NT][2], lo[NT][2];  // P^T, tokens 0..7 and 8..15 of the tile
+            // 8 heads at a time, V's fragments loaded for each: with all 16 heads' P
+            // held at once registers spill (63 us for the 128 lists)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                uint32_t pt[3][2];  // P^T's three parts, tokens 0..7 and 8..15 of the tile
                 const float b0 = m[n][0] == kNegInf ? 0.f : m[n][0], b1 = m[n][1] == kNegInf ? 0.f : m[n][1];
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    const float p0 = exp2_approx(x[n][2 * a] - b0), p1 = exp2_approx(x[n][2 * a + 1] - b1);
-                    l[n][0] += p0;
-                    l[n][1] += p1;
-                    const uint32_t v = pack_bf16x2(p0, p1);
-                    hi[n][a] = movmatrix_trans(v);
-                    lo[n][a] = movmatrix_trans(pack_bf16x2(p0 - bf16_lo_to_f32(v), p1 - bf16_hi_to_f32(v)));
+                    float r0 = exp2_approx(x[n][2 * a] - b0), r1 = exp2_approx(x[n][2 * a + 1] - b1);
+                    l[n][0] += r0;
+                    l[n][1] += r1;
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const uint32_t v = pack_bf16x2(r0, r1);
+                        pt[c][a] = movmatrix_trans(v);
+                        r0 -= bf16_lo_to_f32(v);
+                        r1 -= bf16_hi_to_f32(v);
+                    }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                uint32_t v[4];
-                ldmatrix_x4_trans((v_mat ^ (i << 5)) + stage * kStage, v[0], v[1], v[2], v[3]);
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t v[4];
+                    ldmatrix_x4_trans((v_mat ^ (i << 5)) + stage * kStage, v[0], v[1], v[2], v[3]);
+                    float sum[4] = {};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_bf16_16816(o[n][i], v, hi[n][0], hi[n][1]);
-                    mma_bf16_16816(o[n][i], v, lo[n][0], lo[n][1]);
+                    for (int c = 2; c >= 0; --c) mma_bf16_16816(sum, v, pt[c][0], pt[c][1]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][i][c] += sum[c];
                 }
             }
             __syncwarp();  // every lane has read the stage
