@@ -563,14 +563,16 @@ int pa_select_blocks(const float* scores, int64_t score_stride, const int32_t* c
  *                 a negative entry names no block, and a block listed twice
  *                 counts twice
  *   out           [num_rows][num_q_heads][head_dim], out_dtype PA_F32 or PA_BF16;
- *                 a row that attends to nothing is zero
+ *                 a row that attends to nothing is zero, and so is one whose
+ *                 scores are all -infinity
  * `out` may overlap no other argument.  Deterministic: no atomics, a fixed order
  * of sums (another num_rows or max_selected may split a list differently, within
  * rounding).  Slots at or past L are never used; NaN and infinities of attended
- * tokens spread as in the formula, except that with bf16 inputs an infinite V
- * gives NaN.  An entry at or past the row's blocks, or whose block lies outside
- * [0, num_blocks), is skipped and records PA_ERR_BAD_BLOCK_ID; so is a row with
- * a bad sequence or length (negative, or beyond its table), which gives zeros.
+ * tokens spread as in the formula, except that with bf16 inputs an infinite V may
+ * give NaN for an infinity.  An entry at or past the row's blocks, or whose block
+ * lies outside [0, num_blocks), is skipped and records PA_ERR_BAD_BLOCK_ID; so is
+ * a row with a bad sequence or length (negative, or beyond its table), which gives
+ * zeros.
  * Other arguments as for pa_block_scores.
  */
 int pa_paged_attention_decode_sparse(const void* q, const void* k_pool, const void* v_pool,

@@ -202,7 +202,7 @@ __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r,
 // 2.9e-6 (relative, in norm) below the definition, and is 2.5e-7 off it now, as in
 // the fp32 kernel.  This costs 1 % on streams of long lists (45.7 to 46.3 us), 5 %
 // on one context (6.1 to 6.4 us), 7 % with a group of 16 (51.0 to 54.5 us).
-// (An infinite V meets a remainder of the other sign, or zero, and gives NaN.)
+// (An infinite V that meets a remainder of the other sign, or zero, gives NaN.)
 // Measured: 16 contexts, 64 / 8 heads of 128, 256 blocks of 16 tokens each (269
 // MB): 46.3 us, 5.80 TB/s, 0.88 of a copy, with one CTA on 128 of the 148 SMs;
 // 2048 lists of 64 blocks 160 us, 6.7 TB/s; one context of 128 blocks 6.4 us; a

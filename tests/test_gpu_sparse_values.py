@@ -106,3 +106,65 @@ def test_long_lists_have_no_drift(pa, dtype, group, d):
     off = (out.double() / want - 1).mean().item() * 2.0 ** 24
     assert abs(off) <= 16, off
     assert pa.pa_read_error_flag() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [4, 100])  # one CTA a list, several
+def test_nan_and_infinities_of_attended_tokens(pa, dtype, K):
+    """They go where the formula sends them, and nowhere else."""
+    g = torch.Generator().manual_seed(K)
+    rows, hkv, group, d, bs, L = 7, 2, 4, 64, 16, 60
+    draw = lambda *s: torch.randn(*s, generator=g).to(DT[dtype])
+    tables = torch.randperm(rows * 4 + 2, generator=g)[: rows * 4].reshape(rows, 4)
+    q, kp, vp = draw(rows, hkv * group, d), draw(rows * 4 + 2, hkv, bs, d), draw(rows * 4 + 2, hkv, bs, d)
+    lists = np.full((rows, hkv, K), -1, np.int32)
+    lists[:, :, :3] = [3, 0, 2]                        # block 1 is not attended to
+    nan, inf = float("nan"), float("inf")
+    heads = lambda h: slice(h * group, (h + 1) * group)
+    scale = 0.125
+    clean = rs.sparse_decode(f64(q), f64(kp), f64(vp), tables.tolist(), range(rows), [L] * rows, lists.tolist(), scale)
+    kp[tables[0, 2], 0, 5, 7] = nan                    # row 0, kv head 0: every score's head, all channels
+    vp[tables[1, 0], 1, 3, 9] = nan                    # row 1, kv head 1: one channel
+    vp[tables[2, 3], 0, 11, 20] = inf                  # row 2: the last attended token's value
+    kp[tables[3, 2], 1, 0, 0] = -inf                   # row 3: a score of -inf, a weight of 0
+    q[3, heads(1), 0] = 1.0
+    kp[tables[4, 0], 0, 2, 0], q[4, heads(0), 0] = inf, 0.5   # row 4: a score of +inf
+    q[5, 2, 1] = nan                                   # row 5: one query head
+    for b, h in ((tables[6, 1], 0), (tables[6, 1], 1)):       # row 6: a block that is not listed, and past the length
+        kp[b, h], vp[b, h] = nan, inf
+    kp[tables[6, 3], :, 12:], vp[tables[6, 3], :, 12:] = nan, inf
+    out = f64(attend(pa, q, kp, vp, tables, [L] * rows, lists, scale))
+    with np.errstate(invalid="ignore"):
+        want = rs.sparse_decode(f64(q), f64(kp), f64(vp), tables.tolist(), range(rows), [L] * rows, lists.tolist(), scale)
+    assert np.isnan(want[0, :4]).all() and np.isfinite(want[0, 4:]).all()
+    assert np.isnan(want[1, 4:, 9]).all() and np.isnan(want).sum() == 4 * d + 4 + 4 * d + d
+    assert (want[2, :4, 20] == inf).all() and np.isfinite(want[3]).all() and np.isnan(want[4, :4]).all()
+    if dtype == "bf16":
+        # an infinite V meets the weight's three parts: inf where all are positive, else inf - inf or 0 * inf
+        assert not np.isfinite(out[2, :4, 20]).any() and not (out[2, :4, 20] == -inf).any()
+        out[2, :4, 20] = want[2, :4, 20]
+    finite = np.isfinite(want)
+    assert np.array_equal(np.isnan(out), np.isnan(want)) and np.array_equal(out[np.isinf(want)], want[np.isinf(want)])
+    bar = 1e-5 if dtype == "f32" else 2e-3
+    assert np.abs(out[finite] - want[finite]).max() <= bar and np.array_equal(want[6], clean[6])
+    assert pa.pa_read_error_flag() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [4, 100])
+def test_all_scores_minus_infinity_give_zeros(pa, dtype, K):
+    """No weight is left to share out: such a row is as one that attends to
+    nothing, whichever other rows and heads are finite."""
+    g = torch.Generator().manual_seed(3)
+    draw = lambda *s: torch.randn(*s, generator=g).to(DT[dtype])
+    q, kp, vp = draw(3, 4, 64), draw(9, 2, 8, 64), draw(9, 2, 8, 64)
+    q[:, :, 0] = 1.0
+    tables = torch.arange(9).reshape(3, 3)
+    kp[tables[1], 1, :, 0] = -float("inf")
+    lists = np.full((3, 2, K), -1, np.int32)
+    lists[:, :, 1:4] = [0, 1, 2]
+    out = f64(attend(pa, q, kp, vp, tables, [24, 20, 3], np.where(lists * 8 < np.array([24, 20, 3])[:, None, None], lists, -1), 0.125))
+    assert not out[1, 2:].any()
+    out[1, 2:] = 1.0
+    assert np.isfinite(out).all() and (out != 0).all()
+    assert pa.pa_read_error_flag() == 0
