@@ -540,7 +540,8 @@ int pa_block_scores(const void* q, const void* key_bounds, const int32_t* block_
  * the largest score (NaN counts as largest, equal scores go to the lower
  * block); all of them when the row has no more.  The choice is exact and the
  * same on every run.
- *   scores        float [num_rows][num_kv_heads][score_stride]
+ *   scores        float [num_rows][num_kv_heads][score_stride]; may be NULL when
+ *                 score_stride is 0, with max_context_len 0
  *   context_lens  int32 [num_rows], at most max_context_len
  *   selected      int32 [num_rows][num_kv_heads][max_selected] output: block
  *                 numbers j in ascending order, -1 behind them

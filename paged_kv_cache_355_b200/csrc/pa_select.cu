@@ -987,7 +987,9 @@ extern "C" int pa_select_blocks(const float* scores, int64_t score_stride, const
     if (!supported_block_size(block_size) || num_rows > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     if (score_stride < ((int64_t)max_context_len + block_size - 1) / block_size) return PA_ERR_INVALID_ARG;
     if (num_rows == 0) return PA_OK;
-    if (!scores || !context_lens || !selected || !aligned16(scores) || !aligned16(selected)) return PA_ERR_INVALID_ARG;
+    // scores without columns (max_context_len 0) may have no address: nothing of them is read
+    if ((!scores && score_stride > 0) || !context_lens || !selected || !aligned16(scores) || !aligned16(selected))
+        return PA_ERR_INVALID_ARG;
     const int64_t grid = num_rows * num_kv_heads;
     if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     SelectParams p = {};
