@@ -1,5 +1,5 @@
 """Thin ctypes binding of libpa.so (the shortest calls go through the C module
-_marshal instead of ctypes).
+_marshal instead of ctypes, and fail by its name where it has not been built).
 
 Every function here has the name of the C entry point it calls and only
 marshals arguments: it reads shapes, dtypes and device pointers off torch
@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 
 import torch
 
@@ -24,8 +25,8 @@ _STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_
            4: "PA_ERR_CUDA", 5: "PA_ERR_BAD_BLOCK_ID", 6: "PA_ERR_TIMEOUT"}
 _DTYPES = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
 
-if not all(os.path.exists(p) for p in (LIB_PATH, os.path.join(_HERE, "_marshal.so"))):
-    raise ImportError(f"{LIB_PATH} or _marshal.so is missing: build them with `python -m paged_kv_cache_355_b200.build` "
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m paged_kv_cache_355_b200.build` "
                       "(or __graft_entry__.build()); there is no fallback implementation")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -415,7 +416,11 @@ def pa_paged_attention_prefill(q, k_pool, v_pool, block_tables, context_lens, qu
 # short too: the functions here compare shapes, and _marshal (a C module linked
 # with the same libpa.so) tests every tensor's device, type and layout on the way
 # to the entry point.  They run on their tensors' device, whichever is current.
-from . import _marshal  # noqa: E402  (libpa.so has to be loaded first)
+MARSHAL_PATH = os.path.join(_HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+if os.path.exists(MARSHAL_PATH):
+    from . import _marshal  # libpa.so has to be loaded first
+else:
+    _marshal = None
 
 _ARG_NAMES = {
     "pa_rope_and_cache": "query key value query_stride key_stride value_stride query_out k_pool v_pool slot_mapping "
@@ -431,7 +436,7 @@ _ARG_NAMES = {
     "pa_paged_attention_decode_sparse": "q k_pool v_pool block_tables max_blocks_per_seq seq_ids context_lens selected "
                                         "max_selected scale block_size out",
 }
-_ENTRIES = _marshal.init(torch.int32, torch.int64, torch.float32)
+_ENTRIES = _marshal.init(torch.int32, torch.int64, torch.float32) if _marshal else ()
 _ROPE, _ROPE_DECODE, _BOUNDS, _SCORES, _SELECT, _SPARSE = range(6)
 
 
@@ -459,6 +464,9 @@ def _raw_stream(stream, device: int) -> int:
 
 
 def _call(entry: int, device: int, dtype, args: tuple) -> None:
+    if _marshal is None:
+        raise ImportError(f"{MARSHAL_PATH} is missing: build it with `python -m paged_kv_cache_355_b200.build` (it needs "
+                          "the Python headers); there is no fallback implementation")
     if device < 0 or device == torch.cuda.current_device():  # a tensor that is not on a GPU is refused by name
         status = _marshal.call(entry, device, dtype, args)
     else:

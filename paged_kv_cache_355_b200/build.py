@@ -1,4 +1,4 @@
-"""Build libpa.so (the CUDA kernels and their C ABI) and _marshal.so in-tree for sm_100a.
+"""Build libpa.so (the CUDA kernels and their C ABI) and the _marshal module in-tree for sm_100a.
 
     python -m paged_kv_cache_355_b200.build [--force] [--verbose]
 
@@ -10,8 +10,11 @@ process has loaded.  The same objects, with pa_decode.cu and pa_prefill.cu
 compiled once more with -DPA_TIMELINE, make libpa_timeline.so (per-CTA
 timelines of the decode and prefill kernels, include/pa_timeline.h; read by
 ``python -m paged_kv_cache_355_b200.timeline``).  csrc/pa_marshal.c becomes
-_marshal.so, the CPython module, linked with libpa.so, that the binding's
-shortest calls pass their arguments through.
+the CPython module _marshal, linked with libpa.so, that the binding's shortest
+calls pass their arguments through; its file name carries the interpreter's
+suffix, so that another interpreter never loads it but gets its own.  It needs
+the Python headers; without them the rest is built, and those calls are
+missing.
 """
 from __future__ import annotations
 
@@ -31,7 +34,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 TIMELINE_LIB = os.path.join(PKG, "libpa_timeline.so")
 MARSHAL_SRC = os.path.join(CSRC, "pa_marshal.c")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -92,11 +95,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             tmp = lib + f".tmp{os.getpid()}"
             subprocess.run([nvcc, *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *lib_objs], check=True)
             os.replace(tmp, lib)
-    if force or _mtime(MARSHAL) < max(_mtime(MARSHAL_SRC), newest_header):
+    headers = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers, "Python.h")):
+        sys.stderr.write(f"no Python.h in {headers}: {os.path.basename(MARSHAL)} is not built, and the rotary and "
+                         "block-sparse calls of the Python binding need it\n")
+    elif force or _mtime(MARSHAL) < max(_mtime(MARSHAL_SRC), newest_header):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE, "-I",
-                        sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp, "-L", PKG, "-l:libpa.so",
-                        "-Wl,-rpath,$ORIGIN"], check=True)
+                        headers, MARSHAL_SRC, "-o", tmp, "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"], check=True)
         os.replace(tmp, MARSHAL)
     return LIB
 
