@@ -1,5 +1,5 @@
 """GPU tests of the rotary and block-sparse calls at the ends of their ranges: a
-batch without tokens."""
+batch without tokens, key bounds beyond 32-bit offsets."""
 from __future__ import annotations
 
 import pytest
@@ -42,3 +42,31 @@ def test_a_step_of_empty_sequences(pa):
     # a length that the empty scores cannot hold is flagged, not read
     pa.pa_select_blocks(scores, i32([0, 1, 0]), 0, bs, selected.fill_(9))
     assert (selected == -1).all() and pa.pa_read_error_flag() == 5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_key_bounds_beyond_32_bits(pa, dtype):
+    """Bounds whose own offsets pass 2^32 elements (fp32: 2^31), written and
+    scored at the far end as at the near one."""
+    hkv, bs, d = 8, 8, 128
+    NB = ((1 << 32) if dtype == torch.bfloat16 else (1 << 31)) // (hkv * 2 * d) + 9
+    # 34 GB of keys; only the used blocks are written
+    kp = torch.empty(NB, hkv, bs, d, dtype=dtype, device="cuda")
+    kb = torch.empty(NB, hkv, 2, d, dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    keys = torch.randn(3, hkv, bs, d, generator=g, device="cuda").to(dtype)
+    q = torch.randn(1, 2 * hkv, d, generator=g, device="cuda").to(dtype)
+    near, far = [2, 0, 1], [NB - 1, NB // 2 + 1, NB - 7]
+    got = []
+    for blocks in (far, near):
+        at = torch.tensor(blocks, device="cuda")
+        kp[at], kb[at] = keys, 0
+        lens, tables = i32([2 * bs + 5]), i32([blocks])
+        pa.pa_update_key_bounds(kp, kb, tables, lens, query_start=i32([0, 2 * bs + 5]), max_query_len=2 * bs + 5)
+        scores = torch.full((1, hkv, 3), -7.0, device="cuda")
+        pa.pa_block_scores(q, kb, tables, lens, 2 * bs + 5, bs, scores)
+        assert torch.equal(kb[at][:2], torch.stack([keys[:2].amin(2), keys[:2].amax(2)], 2))
+        assert torch.equal(kb[at][2], torch.stack([keys[2, :, :5].amin(1), keys[2, :, :5].amax(1)], 1))
+        got.append(scores)
+    assert torch.equal(*got) and (got[0] != -7).all()
+    assert pa.pa_read_error_flag() == 0
