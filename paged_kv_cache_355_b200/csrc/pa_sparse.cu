@@ -46,8 +46,8 @@ __device__ __forceinline__ void store_out(const SparseParams& p, int64_t at, flo
 
 // Warps of a CTA, each with a ring of 16 KB.  bf16: six, two CTAs an SM, while
 // all lists' CTAs fit the GPU at once, else four, three CTAs an SM, which end
-// more evenly (256 lists of 128 blocks of 16 tokens: 46 us with six, 51 with
-// four; 320 of 64: 37.8 and 33.4; 2048 of 16: 55 and 47.6).  fp32: twelve, one
+// more evenly (256 lists of 128 blocks of 16 tokens: 47.0 us with six, 52.1 with
+// four; 320 of 64: 38.3 and 32.4; 2048 of 16: 61.5 and 51.1).  fp32: twelve, one
 // CTA an SM, since a warp computes longer on what it has (128 lists of 128: 50
 // us; with four warps and each list split in three, 53).
 constexpr int kF32Warps = 12;
@@ -201,11 +201,11 @@ __device__ __forceinline__ void join_states(const SparseParams& p, const Row& r,
 // does not fit its sum: through a running sum of 43 tiles a warp, an fp32 output was
 // 2.9e-6 (relative, in norm) below the definition, and is 2.5e-7 off it now, as in
 // the fp32 kernel.  This costs 1 % on streams of long lists (45.7 to 46.3 us), 5 %
-// on one context (6.1 to 6.4 us), 7 % with a group of 16 (51.0 to 54.5 us).
+// on one context (6.1 to 6.5 us), 7 % with a group of 16 (51.0 to 54.5 us).
 // (An infinite V that meets a remainder of the other sign, or zero, gives NaN.)
 // Measured: 16 contexts, 64 / 8 heads of 128, 256 blocks of 16 tokens each (269
 // MB): 46.3 us, 5.80 TB/s, 0.88 of a copy, with one CTA on 128 of the 148 SMs;
-// 2048 lists of 64 blocks 160 us, 6.7 TB/s; one context of 128 blocks 6.4 us; a
+// 2048 lists of 64 blocks 160 us, 6.7 TB/s; one context of 128 blocks 6.5 us; a
 // group of 16, 128 lists of 256 blocks, 4.9 TB/s.
 // One cluster of `splits` CTAs per (row, kv head): its splits * WARPS warps take
 // the tiles of the list in turn, each with its own running maximum and sum, and
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) sparse_mma_kernel(cons
 // time: the products of 4 G scores are summed over the lanes by one
 // reduce-scatter (about 4 G shuffles instead of 4 G log2(D / 4)), so that each
 // weight is computed by one lane or few, and reaches the others through shared
-// memory.  Measured: 128 lists of 128 blocks of 16 tokens, D 128: one query head
-// 5.9 TB/s, eight 5.4 TB/s.
+// memory.  Measured: 128 equal lists of 128 blocks of 16 tokens, D 128: one query
+// head 6.0 TB/s, eight 5.4 TB/s.
 template <int D, int G, int kStages>
 __global__ void __launch_bounds__(kF32Warps * 32, 1) sparse_f32_kernel(const SparseParams p, int splits) {
     constexpr int kLanes = D / 4;
@@ -592,9 +592,9 @@ int launch_sparse(const SparseParams& p, void (*kernel)(SparseParams, int), std:
     // half-tiles are counted in 32 bits (a pool that needs more is 4 TB)
     if (p.num_blocks > (1ll << 32) / (p.num_kv_heads * (p.block_size / 8))) return PA_ERR_UNSUPPORTED;
     // One CTA a list keeps its warps longest in their stream: at 128 lists of 256
-    // blocks of 16 tokens 45.3 us, against 48.2 with two and 52.8 with three.
+    // blocks of 16 tokens 46.3 us, against 48.9 with two and 54.1 with three.
     // Fewer lists are split over as many CTAs as leave each SM one (64 lists of
-    // 128 blocks: 19.5 us with one, 17.8 with two; 8 lists: 15.1 with one, 6.7
+    // 128 blocks: 20.7 us with one, 18.1 with two; 8 lists: 17.3 with one, 6.5
     // with eight).
     const int64_t steps = ((int64_t)p.max_selected * p.block_size + step_tokens - 1) / step_tokens;
     int64_t splits = std::min(num_sms() / units, std::min((int64_t)kMaxSplits, (steps + warps - 1) / warps));
